@@ -15,11 +15,12 @@ LIB_PATH = os.path.join(HERE, "librtvla.so")
 
 ENGINE_AUTO, ENGINE_LAYERED, ENGINE_PERSISTENT = 0, 1, 2
 VARIANT_PI05, VARIANT_PI0 = 0, 1
+DTYPE_BF16, DTYPE_F16, DTYPE_F32 = 0, 1, 2
 
 STATUS = {
     0: "RTVLA_OK", 1: "RTVLA_ERR_INVALID_ARG", 2: "RTVLA_ERR_SHAPE", 3: "RTVLA_ERR_MASK_NOT_PREFIX",
     4: "RTVLA_ERR_OOM", 5: "RTVLA_ERR_CUDA", 6: "RTVLA_ERR_DEVICE_TIMEOUT", 7: "RTVLA_ERR_UNSUPPORTED",
-    8: "RTVLA_ERR_DEVICE_BOUNDS", 9: "RTVLA_ERR_GUARD_OVERWRITE",
+    8: "RTVLA_ERR_DEVICE_BOUNDS", 9: "RTVLA_ERR_GUARD_OVERWRITE", 10: "RTVLA_ERR_NO_PAGES",
 }
 
 # the symbols include/rtvla.h declares
@@ -31,6 +32,8 @@ EXPORTS = (
     "rtvla_sample_actions_pi0", "rtvla_debug_trace_pi0",
     "rtvla_vision_create", "rtvla_encode_images", "rtvla_vision_debug_trace", "rtvla_vision_sync_status",
     "rtvla_vision_kernels_per_call", "rtvla_vision_destroy",
+    "rtvla_pages_create", "rtvla_pages_plan", "rtvla_pages_write", "rtvla_pages_attend", "rtvla_pages_select",
+    "rtvla_pages_sync_status", "rtvla_pages_destroy",
 )
 
 
@@ -86,6 +89,16 @@ class RtvlaKV(ctypes.Structure):
     _fields_ = [("k", _P), ("v", _P), ("valid_len", _P), ("batch", ctypes.c_int), ("prefix_cap", ctypes.c_int)]
 
 
+class RtvlaPagesConfig(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int) for n in (
+        "dtype", "n_layers", "n_q_heads", "n_kv_heads", "head_dim", "page_size", "n_pages", "table_width",
+        "max_batch", "has_select")] + [("rope_theta", ctypes.c_float)]
+
+
+class RtvlaPagedKV(ctypes.Structure):
+    _fields_ = [("k", _P), ("v", _P), ("k_mean", _P), ("table", _P), ("lens", _P), ("batch", ctypes.c_int)]
+
+
 _LIB = None
 
 
@@ -121,11 +134,21 @@ def _lib():
         lib.rtvla_vision_kernels_per_call.argtypes = [_P, ctypes.c_int]
         lib.rtvla_vision_destroy.argtypes = [_P]
         lib.rtvla_vision_destroy.restype = None
+        _KV = ctypes.POINTER(RtvlaPagedKV)
+        lib.rtvla_pages_create.argtypes = [ctypes.POINTER(RtvlaPagesConfig), ctypes.POINTER(_P)]
+        lib.rtvla_pages_plan.argtypes = [_P, _P, _P, _P, _P, _KV, _P, _P, _P, _P, ctypes.c_int, _P]
+        lib.rtvla_pages_write.argtypes = [_P, ctypes.c_int, _P, ctypes.c_int, _P, _P, ctypes.c_int, _KV, _P, _P]
+        lib.rtvla_pages_attend.argtypes = [_P, ctypes.c_int, _P, _KV, _P, ctypes.c_int, _P, _P]
+        lib.rtvla_pages_select.argtypes = [_P, ctypes.c_int, _P, _KV, ctypes.c_int, ctypes.c_int, ctypes.c_int, _P,
+                                           _P]
+        lib.rtvla_pages_sync_status.argtypes = [_P, _P]
+        lib.rtvla_pages_destroy.argtypes = [_P]
+        lib.rtvla_pages_destroy.restype = None
         lib.rtvla_status_string.argtypes = [ctypes.c_int]
         lib.rtvla_status_string.restype = ctypes.c_char_p
         for n in EXPORTS:
             if n not in ("rtvla_kv_bytes", "rtvla_destroy", "rtvla_status_string", "rtvla_kernels_per_call",
-                         "rtvla_vision_destroy", "rtvla_vision_kernels_per_call"):
+                         "rtvla_vision_destroy", "rtvla_vision_kernels_per_call", "rtvla_pages_destroy"):
                 getattr(lib, n).restype = ctypes.c_int
         lib.rtvla_kernels_per_call.restype = ctypes.c_int
         lib.rtvla_vision_kernels_per_call.restype = ctypes.c_int
@@ -214,6 +237,18 @@ def make_vision_weights(w: dict, n_layers: int):
         keep.append(arr)
         setattr(ws, n, ctypes.cast(arr, _PP))
     return ws, keep
+
+
+def make_pages_config(n_pages, table_width, page_size=16, dtype=DTYPE_BF16, n_layers=18, n_q_heads=8, n_kv_heads=1,
+                      head_dim=256, max_batch=1, has_select=True, rope_theta=10000.0) -> RtvlaPagesConfig:
+    """rtvla_pages_config; the defaults are the prefix model's heads (8 x 256 on one KV head)."""
+    return RtvlaPagesConfig(dtype=dtype, n_layers=n_layers, n_q_heads=n_q_heads, n_kv_heads=n_kv_heads,
+                            head_dim=head_dim, page_size=page_size, n_pages=n_pages, table_width=table_width,
+                            max_batch=max_batch, has_select=int(bool(has_select)), rope_theta=rope_theta)
+
+
+def make_paged_kv(k, v, k_mean, table, lens, batch: int) -> RtvlaPagedKV:
+    return RtvlaPagedKV(k=_ptr(k), v=_ptr(v), k_mean=_ptr(k_mean), table=_ptr(table), lens=_ptr(lens), batch=batch)
 
 
 def make_kv(k, v, valid_len, batch: int, prefix_cap: int) -> RtvlaKV:
@@ -340,3 +375,46 @@ def rtvla_vision_kernels_per_call(ctx: int, n_images: int) -> int:
 def rtvla_vision_destroy(ctx: int):
     if ctx:
         _lib().rtvla_vision_destroy(ctx)
+
+
+# ---------------------------------------------------------------------------------------
+# paged KV cache
+
+def rtvla_pages_create(cfg: RtvlaPagesConfig) -> int:
+    out = _P()
+    _check(_lib().rtvla_pages_create(ctypes.byref(cfg), ctypes.byref(out)), "rtvla_pages_create")
+    return out.value
+
+
+def rtvla_pages_plan(ctx: int, lens, delta, free_pages, n_free, kv: RtvlaPagedKV, n_free_out, slots, positions,
+                     row_start, n_rows: int, stream=None):
+    _check(_lib().rtvla_pages_plan(ctx, _ptr(lens), _ptr(delta), _ptr(free_pages), _ptr(n_free), ctypes.byref(kv),
+                                   _ptr(n_free_out), _ptr(slots), _ptr(positions), _ptr(row_start), n_rows,
+                                   _stream(stream)), "rtvla_pages_plan")
+
+
+def rtvla_pages_write(ctx: int, layer: int, qkv, qkv_dtype: int, slots, positions, n_rows: int, kv: RtvlaPagedKV,
+                      q_out, stream=None):
+    _check(_lib().rtvla_pages_write(ctx, layer, _ptr(qkv), qkv_dtype, _ptr(slots), _ptr(positions), n_rows,
+                                    ctypes.byref(kv), _ptr(q_out), _stream(stream)), "rtvla_pages_write")
+
+
+def rtvla_pages_attend(ctx: int, layer: int, q, kv: RtvlaPagedKV, sel, sel_width: int, out, stream=None):
+    _check(_lib().rtvla_pages_attend(ctx, layer, _ptr(q), ctypes.byref(kv), _ptr(sel), sel_width, _ptr(out),
+                                     _stream(stream)), "rtvla_pages_attend")
+
+
+def rtvla_pages_select(ctx: int, layer: int, q, kv: RtvlaPagedKV, budget: int, keep_first: int, keep_last: int, sel,
+                       stream=None):
+    _check(_lib().rtvla_pages_select(ctx, layer, _ptr(q), ctypes.byref(kv), budget, keep_first, keep_last, _ptr(sel),
+                                     _stream(stream)), "rtvla_pages_select")
+
+
+def rtvla_pages_sync_status(ctx: int, stream=None) -> int:
+    """Returns the device status code (0 = ok); does not raise."""
+    return _lib().rtvla_pages_sync_status(ctx, _stream(stream))
+
+
+def rtvla_pages_destroy(ctx: int):
+    if ctx:
+        _lib().rtvla_pages_destroy(ctx)

@@ -14,7 +14,7 @@ typedef __nv_bfloat16 bf16;
 
 // ---------------------------------------------------------------------------------------
 // device error word (read and cleared by rtvla_sync_status)
-enum : int { DEVERR_TIMEOUT = 1, DEVERR_BOUNDS = 2, DEVERR_MASK = 4, DEVERR_GUARD = 8 };
+enum : int { DEVERR_TIMEOUT = 1, DEVERR_BOUNDS = 2, DEVERR_MASK = 4, DEVERR_GUARD = 8, DEVERR_NO_PAGES = 16 };
 
 struct DevCtl {
   int err;                       // OR of DEVERR_*

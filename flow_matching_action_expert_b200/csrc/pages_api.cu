@@ -1,0 +1,288 @@
+// C ABI of the paged KV cache (rtvla_pages_*): argument checks, the context with its RoPE tables
+// and workspaces, and the launches.
+#include <cmath>
+#include <cstdlib>
+#include <cstring>
+#include <new>
+#include <vector>
+
+#include "kernels.h"
+#include "pages.h"
+#include "rtvla.h"
+
+using namespace rtvla;
+
+struct rtvla_pages_ctx {
+  rtvla_pages_config cfg;
+  PageGeom g;
+  int device = 0, sm_count = 148;
+  std::vector<void *> allocs;
+  size_t mem_cap = 0, mem_used = 0;
+  bool checked = false;
+  std::vector<GuardRegion> guards;
+  GuardRegion *d_guards = nullptr;
+  DevCtl *ctl = nullptr;
+  float2 *rope_lo = nullptr, *rope_hi = nullptr;
+  unsigned long long *keys = nullptr;  // select: [max_batch][n_kv_heads][table_width]
+};
+
+namespace {
+
+// Makes the context's device current for a call and restores the caller's.
+struct OnDevice {
+  int before = -1, want;
+  bool ok;
+  explicit OnDevice(int device) : want(device) {
+    ok = cudaGetDevice(&before) == cudaSuccess && (before == want || cudaSetDevice(want) == cudaSuccess);
+  }
+  ~OnDevice() {
+    if (ok && before != want) cudaSetDevice(before);
+  }
+};
+
+// Allocation with the context's memory cap and, in checked mode, guard bands (as the denoise
+// context's buffers).
+template <typename T>
+T *p_alloc(rtvla_pages_ctx *c, size_t n) {
+  void *p = nullptr;
+  const size_t bytes = (n * sizeof(T) + 255) & ~size_t(255);
+  const size_t total = c->checked ? bytes + 2 * (size_t)GUARD_BYTES : bytes;
+  if (c->mem_cap && c->mem_used + total > c->mem_cap) return nullptr;
+  if (cudaMalloc(&p, total) != cudaSuccess) {
+    cudaGetLastError();
+    return nullptr;
+  }
+  c->allocs.push_back(p);
+  c->mem_used += total;
+  if (!c->checked) return static_cast<T *>(p);
+  unsigned char *b = static_cast<unsigned char *>(p);
+  if (cudaMemset(b, GUARD_FILL, GUARD_BYTES) != cudaSuccess ||
+      cudaMemset(b + GUARD_BYTES + bytes, GUARD_FILL, GUARD_BYTES) != cudaSuccess) {
+    cudaGetLastError();
+    return nullptr;
+  }
+  c->guards.push_back(GuardRegion{b, (unsigned long long)bytes});
+  return reinterpret_cast<T *>(b + GUARD_BYTES);
+}
+
+void p_free(rtvla_pages_ctx *c) {
+  for (void *p : c->allocs) cudaFree(p);
+  if (c->d_guards) cudaFree(c->d_guards);
+  delete c;
+}
+
+rtvla_status check_cfg(const rtvla_pages_config *g) {
+  if (g->n_layers < 1 || g->n_layers > 256 || g->n_q_heads < 1 || g->n_kv_heads < 1 || g->n_kv_heads > 64 ||
+      g->page_size < 1 || g->n_pages < 1 || g->table_width < 1 || g->max_batch < 1 || g->max_batch > 4096 ||
+      !(g->rope_theta >= 0.f) || !std::isfinite(g->rope_theta))
+    return RTVLA_ERR_INVALID_ARG;
+  if ((long long)g->n_pages * g->page_size >= (1ll << 31) || (long long)g->table_width * g->page_size > (1ll << 24))
+    return RTVLA_ERR_INVALID_ARG;
+  if (g->n_q_heads % g->n_kv_heads) return RTVLA_ERR_INVALID_ARG;
+  if (g->dtype != RTVLA_DTYPE_BF16 && g->dtype != RTVLA_DTYPE_F16) return RTVLA_ERR_UNSUPPORTED;
+  if (g->head_dim != 64 && g->head_dim != 128 && g->head_dim != 256) return RTVLA_ERR_UNSUPPORTED;
+  if (g->n_q_heads / g->n_kv_heads > 16) return RTVLA_ERR_UNSUPPORTED;
+  if (g->page_size > 1024 || (g->page_size & (g->page_size - 1))) return RTVLA_ERR_UNSUPPORTED;
+  return RTVLA_OK;
+}
+
+// (cos, sin) of positions step * i, angle = position * theta^(-2j/d) in fp64, rounded once
+rtvla_status build_rope(float2 *dst, int rows, int step, int d, double theta) {
+  std::vector<float2> t((size_t)rows * (d / 2));
+  for (int i = 0; i < rows; ++i)
+    for (int j = 0; j < d / 2; ++j) {
+      const double a = (double)i * step * std::pow(theta, -2.0 * j / d);
+      t[(size_t)i * (d / 2) + j] = make_float2((float)std::cos(a), (float)std::sin(a));
+    }
+  return cudaMemcpy(dst, t.data(), t.size() * sizeof(float2), cudaMemcpyHostToDevice) == cudaSuccess
+             ? RTVLA_OK
+             : RTVLA_ERR_CUDA;
+}
+
+rtvla_status p_create(rtvla_pages_ctx *c) {
+  const rtvla_pages_config &g = c->cfg;
+  if (cudaGetDevice(&c->device) != cudaSuccess ||
+      cudaDeviceGetAttribute(&c->sm_count, cudaDevAttrMultiProcessorCount, c->device) != cudaSuccess)
+    return RTVLA_ERR_CUDA;
+  if (pages_init_attributes() != cudaSuccess) return RTVLA_ERR_CUDA;
+  c->ctl = p_alloc<DevCtl>(c, 1);
+  if (!c->ctl) return RTVLA_ERR_OOM;
+  if (g.rope_theta > 0.f) {
+    const int hi = ((g.table_width * g.page_size - 1) >> 8) + 1;
+    c->rope_lo = p_alloc<float2>(c, (size_t)256 * (g.head_dim / 2));
+    c->rope_hi = p_alloc<float2>(c, (size_t)hi * (g.head_dim / 2));
+    if (!c->rope_lo || !c->rope_hi) return RTVLA_ERR_OOM;
+    if (build_rope(c->rope_lo, 256, 1, g.head_dim, g.rope_theta) != RTVLA_OK ||
+        build_rope(c->rope_hi, hi, 256, g.head_dim, g.rope_theta) != RTVLA_OK)
+      return RTVLA_ERR_CUDA;
+  }
+  if (g.has_select) {
+    c->keys = p_alloc<unsigned long long>(c, (size_t)g.max_batch * g.n_kv_heads * g.table_width);
+    if (!c->keys) return RTVLA_ERR_OOM;
+  }
+  DevCtl hc;
+  std::memset(&hc, 0, sizeof(hc));
+  if (cudaMemcpy(c->ctl, &hc, sizeof(hc), cudaMemcpyHostToDevice) != cudaSuccess) return RTVLA_ERR_CUDA;
+  if (c->checked) {
+    const size_t b = c->guards.size() * sizeof(GuardRegion);
+    if (cudaMalloc(&c->d_guards, b) != cudaSuccess ||
+        cudaMemcpy(c->d_guards, c->guards.data(), b, cudaMemcpyHostToDevice) != cudaSuccess)
+      return RTVLA_ERR_CUDA;
+  }
+  return cudaDeviceSynchronize() == cudaSuccess ? RTVLA_OK : RTVLA_ERR_CUDA;
+}
+
+bool aligned(const void *p, size_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
+
+// the parts of the cache a per-layer call reads
+rtvla_status check_kv(const rtvla_pages_ctx *c, int layer, const rtvla_paged_kv *kv) {
+  if (!c || !kv || !kv->k || !kv->v || !aligned(kv->k, 16) || !aligned(kv->v, 16) || !aligned(kv->k_mean, 16) ||
+      layer < 0)
+    return RTVLA_ERR_INVALID_ARG;
+  return layer < c->cfg.n_layers ? RTVLA_OK : RTVLA_ERR_SHAPE;
+}
+
+rtvla_status check_requests(const rtvla_pages_ctx *c, const rtvla_paged_kv *kv) {
+  if (!kv->table || !kv->lens || !aligned(kv->table, 4) || !aligned(kv->lens, 4) || kv->batch < 1)
+    return RTVLA_ERR_INVALID_ARG;
+  return kv->batch <= c->cfg.max_batch ? RTVLA_OK : RTVLA_ERR_SHAPE;
+}
+
+rtvla_status launched(cudaError_t e) {
+  if (e == cudaSuccess) return RTVLA_OK;
+  cudaGetLastError();
+  return RTVLA_ERR_CUDA;
+}
+
+}  // namespace
+
+// =======================================================================================
+// C ABI
+
+extern "C" {
+
+rtvla_status rtvla_pages_create(const rtvla_pages_config *cfg, rtvla_pages_ctx **out) {
+  if (!cfg || !out) return RTVLA_ERR_INVALID_ARG;
+  *out = nullptr;
+  rtvla_status st = check_cfg(cfg);
+  if (st != RTVLA_OK) return st;
+  rtvla_pages_ctx *c = new (std::nothrow) rtvla_pages_ctx();
+  if (!c) return RTVLA_ERR_OOM;
+  c->cfg = *cfg;
+  c->g = PageGeom{0, cfg->n_pages, cfg->table_width, cfg->n_kv_heads, cfg->head_dim};
+  while ((1 << c->g.shift) < cfg->page_size) ++c->g.shift;
+  if (const char *env = std::getenv("RTVLA_CHECKED")) c->checked = std::atoi(env) != 0;
+  if (const char *env = std::getenv("RTVLA_DEVICE_MEMORY_CAP")) c->mem_cap = (size_t)std::strtoull(env, nullptr, 10);
+  try {
+    st = p_create(c);
+  } catch (const std::bad_alloc &) {
+    st = RTVLA_ERR_OOM;
+  }
+  if (st != RTVLA_OK) {
+    cudaGetLastError();
+    p_free(c);
+    return st;
+  }
+  *out = c;
+  return RTVLA_OK;
+}
+
+rtvla_status rtvla_pages_plan(rtvla_pages_ctx *c, const int32_t *lens, const int32_t *delta, int32_t *free_pages,
+                              const int32_t *n_free, const rtvla_paged_kv *kv, int32_t *n_free_out, int32_t *slots,
+                              int32_t *positions, int32_t *row_start, int n_rows, void *stream) {
+  if (!c || !lens || !delta || !free_pages || !n_free || !kv || !n_free_out || !row_start || n_rows < 0 ||
+      (n_rows > 0 && (!slots || !positions)))
+    return RTVLA_ERR_INVALID_ARG;
+  const void *ints[] = {lens, delta, free_pages, n_free, n_free_out, slots, positions, row_start};
+  for (const void *p : ints)
+    if (!aligned(p, 4)) return RTVLA_ERR_INVALID_ARG;
+  const rtvla_status s = check_requests(c, kv);
+  if (s != RTVLA_OK) return s;
+  if (n_rows > (1 << 24)) return RTVLA_ERR_SHAPE;
+  OnDevice dev(c->device);
+  if (!dev.ok) return RTVLA_ERR_CUDA;
+  PlanParams p{c->g,     lens,       delta, free_pages, n_free,    kv->table, kv->lens,
+               n_free_out, slots, positions, row_start, kv->batch, n_rows, c->ctl};
+  return launched(launch_pages_plan(p, static_cast<cudaStream_t>(stream)));
+}
+
+rtvla_status rtvla_pages_write(rtvla_pages_ctx *c, int layer, const void *qkv, int qkv_dtype, const int32_t *slots,
+                               const int32_t *positions, int n_rows, const rtvla_paged_kv *kv, void *q_out,
+                               void *stream) {
+  const rtvla_status s = check_kv(c, layer, kv);
+  if (s != RTVLA_OK) return s;
+  if (n_rows < 0 || (qkv_dtype != c->cfg.dtype && qkv_dtype != RTVLA_DTYPE_F32)) return RTVLA_ERR_INVALID_ARG;
+  if (n_rows > 0 && (!qkv || !slots || !positions || !q_out || !aligned(qkv, 16) || !aligned(q_out, 16) ||
+                     !aligned(slots, 4) || !aligned(positions, 4)))
+    return RTVLA_ERR_INVALID_ARG;
+  if (n_rows > (1 << 24)) return RTVLA_ERR_SHAPE;
+  OnDevice dev(c->device);
+  if (!dev.ok) return RTVLA_ERR_CUDA;
+  WriteParams p{c->g, layer, c->cfg.n_q_heads, n_rows, qkv,        slots,      positions,
+                kv->k, kv->v, kv->k_mean,      q_out,  c->rope_lo, c->rope_hi, c->ctl};
+  return launched(launch_pages_write(p, c->cfg.dtype, qkv_dtype, static_cast<cudaStream_t>(stream)));
+}
+
+rtvla_status rtvla_pages_attend(rtvla_pages_ctx *c, int layer, const void *q, const rtvla_paged_kv *kv,
+                                const int32_t *sel, int sel_width, void *out, void *stream) {
+  rtvla_status s = check_kv(c, layer, kv);
+  if (s == RTVLA_OK) s = check_requests(c, kv);
+  if (s != RTVLA_OK) return s;
+  if (!q || !out || !aligned(q, 16) || !aligned(out, 16) || !aligned(sel, 4) || (sel && sel_width < 1))
+    return RTVLA_ERR_INVALID_ARG;
+  if (sel && sel_width > 65536) return RTVLA_ERR_SHAPE;
+  OnDevice dev(c->device);
+  if (!dev.ok) return RTVLA_ERR_CUDA;
+  PagedAttnParams p{c->g,      layer, c->cfg.n_q_heads,   kv->batch, q, kv->k, kv->v, kv->table, kv->lens, sel,
+                    sel_width, out,   (float)(1.4426950408889634 / std::sqrt((double)c->cfg.head_dim)), c->ctl};
+  return launched(launch_pages_attend(p, c->cfg.dtype, static_cast<cudaStream_t>(stream)));
+}
+
+rtvla_status rtvla_pages_select(rtvla_pages_ctx *c, int layer, const void *q, const rtvla_paged_kv *kv, int budget,
+                                int keep_first, int keep_last, int32_t *sel, void *stream) {
+  rtvla_status s = check_kv(c, layer, kv);
+  if (s == RTVLA_OK) s = check_requests(c, kv);
+  if (s != RTVLA_OK) return s;
+  if (!q || !kv->k_mean || !sel || !aligned(q, 16) || !aligned(sel, 4) || keep_first < 0 || keep_last < 1 ||
+      (long long)keep_first + keep_last > budget)
+    return RTVLA_ERR_INVALID_ARG;
+  if (budget > 65536) return RTVLA_ERR_SHAPE;
+  if (!c->keys) return RTVLA_ERR_UNSUPPORTED;
+  OnDevice dev(c->device);
+  if (!dev.ok) return RTVLA_ERR_CUDA;
+  SelectParams p{c->g,     layer,    c->cfg.n_q_heads, kv->batch, q,       kv->k_mean, kv->table,
+                 kv->lens, budget, keep_first,       keep_last, sel, c->keys,    c->ctl};
+  return launched(launch_pages_select(p, c->cfg.dtype, static_cast<cudaStream_t>(stream)));
+}
+
+rtvla_status rtvla_pages_sync_status(rtvla_pages_ctx *c, void *stream) {
+  if (!c) return RTVLA_ERR_INVALID_ARG;
+  OnDevice dev(c->device);
+  if (!dev.ok) return RTVLA_ERR_CUDA;
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  if (c->checked && launch_check_guards(c->d_guards, (int)c->guards.size(), c->ctl, st) != cudaSuccess) {
+    cudaGetLastError();
+    return RTVLA_ERR_CUDA;
+  }
+  if (cudaStreamSynchronize(st) != cudaSuccess) {
+    cudaGetLastError();
+    return RTVLA_ERR_CUDA;
+  }
+  DevCtl h;
+  if (cudaMemcpy(&h, c->ctl, sizeof(h), cudaMemcpyDeviceToHost) != cudaSuccess) return RTVLA_ERR_CUDA;
+  if (h.err == 0) return RTVLA_OK;
+  const int zero[2] = {0, 0};
+  if (cudaMemcpy(c->ctl, zero, sizeof(zero), cudaMemcpyHostToDevice) != cudaSuccess) return RTVLA_ERR_CUDA;
+  if (h.err & DEVERR_GUARD) return RTVLA_ERR_GUARD_OVERWRITE;
+  if (h.err & DEVERR_BOUNDS) return RTVLA_ERR_DEVICE_BOUNDS;
+  return RTVLA_ERR_NO_PAGES;
+}
+
+void rtvla_pages_destroy(rtvla_pages_ctx *c) {
+  if (!c) return;
+  OnDevice dev(c->device);
+  cudaDeviceSynchronize();
+  p_free(c);
+}
+
+}  // extern "C"

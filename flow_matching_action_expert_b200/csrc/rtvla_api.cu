@@ -916,6 +916,7 @@ const char *rtvla_status_string(rtvla_status s) {
     case RTVLA_ERR_UNSUPPORTED: return "unsupported model shape or engine";
     case RTVLA_ERR_DEVICE_BOUNDS: return "a valid length exceeded its buffer";
     case RTVLA_ERR_GUARD_OVERWRITE: return "a guard band around a library buffer was overwritten";
+    case RTVLA_ERR_NO_PAGES: return "the paged cache's free list ran out";
   }
   return "unknown status";
 }

@@ -48,7 +48,8 @@ typedef enum {
   RTVLA_ERR_DEVICE_TIMEOUT = 6,  /* a bounded device-side wait expired (device-detected) */
   RTVLA_ERR_UNSUPPORTED = 7,     /* model shape the kernels are not built for */
   RTVLA_ERR_DEVICE_BOUNDS = 8,   /* a valid length exceeded its buffer (device-detected, clamped) */
-  RTVLA_ERR_GUARD_OVERWRITE = 9  /* checked mode: a guard band around a library buffer changed */
+  RTVLA_ERR_GUARD_OVERWRITE = 9, /* checked mode: a guard band around a library buffer changed */
+  RTVLA_ERR_NO_PAGES = 10        /* a paged cache's free list ran out (device-detected) */
 } rtvla_status;
 
 /* Engines that run the denoise loop (rtvla_config.engine).  The persistent engine applies to
@@ -427,6 +428,141 @@ int rtvla_vision_kernels_per_call(rtvla_vision_ctx *ctx, int n_images);
 
 /* Frees everything the context owns (waits for the device first).  NULL is a no-op. */
 void rtvla_vision_destroy(rtvla_vision_ctx *ctx);
+
+/* =========================================================================================
+ * Paged KV cache: one pool of fixed-size pages shared by requests of different length, the
+ * bookkeeping that hands its pages out, and the attention of one new token per request over it.
+ * The pages' pipeline fills a contiguous rtvla_kv once and attends into it; these calls serve
+ * what comes next to that: text decoding of the prefix model, an observation appended to a
+ * prefix, robots with long histories that share one GPU's memory (integration aids of this
+ * library; the paper has no counterpart).  A context of its own, with the conventions above
+ * (contiguous row-major tensors, asynchronous calls on `stream`, device-detected errors through
+ * a sync call; calls on one context must not overlap on the GPU).
+ *
+ * A request b holds lens[b] tokens.  Token t lives in slot table[b][t / page_size] * page_size +
+ * t % page_size of the pool.  Pages hold keys after RoPE ("rotate half" pairs (d, d + head_dim/2),
+ * token t at position t), as rtvla_kv does: an rtvla_kv of capacity P is itself a pool with
+ * batch * P / page_size pages whose table is table[b][i] = b * P / page_size + i, if page_size
+ * divides P.
+ *
+ * One step:  rtvla_pages_plan (pages, slots and positions of the new tokens); then per layer
+ * rtvla_pages_write (the new tokens' Q, K, V), rtvla_pages_attend, or rtvla_pages_select and
+ * rtvla_pages_attend on its list.  rtvla_prefix_step runs all layers of the prefix model so.
+ * ========================================================================================= */
+typedef struct rtvla_pages_ctx rtvla_pages_ctx; /* opaque; owned by the library */
+
+enum {
+  RTVLA_DTYPE_BF16 = 0,
+  RTVLA_DTYPE_F16 = 1, /* IEEE half */
+  RTVLA_DTYPE_F32 = 2  /* qkv rows of rtvla_pages_write only */
+};
+
+typedef struct {
+  int dtype;        /* of the cache, queries and outputs: RTVLA_DTYPE_BF16 or _F16 */
+  int n_layers;     /* 1..256 */
+  int n_q_heads;    /* a multiple of n_kv_heads, at most 16 times it; head h reads KV head
+                       h / (n_q_heads / n_kv_heads) */
+  int n_kv_heads;   /* 1..64 */
+  int head_dim;     /* 64, 128 or 256 */
+  int page_size;    /* tokens per page: a power of two, 1..1024 */
+  int n_pages;      /* pages in the pool; n_pages * page_size < 2^31 */
+  int table_width;  /* pages one request can hold; table_width * page_size <= 2^24 */
+  int max_batch;    /* 1..4096 */
+  int has_select;   /* 1: allocate rtvla_pages_select's workspace, 8 bytes per request, KV head and
+                       table entry */
+  float rope_theta; /* RoPE base; 0: rtvla_pages_write does not rotate */
+} rtvla_pages_config;
+
+/* The cache (caller-owned device memory; k, v and k_mean 16-byte aligned). */
+typedef struct {
+  void *k;         /* [n_layers][n_pages][n_kv_heads][page_size][head_dim] */
+  void *v;         /* the same */
+  void *k_mean;    /* [n_layers][n_pages][n_kv_heads][head_dim]: mean key of every full page; may be
+                      null when rtvla_pages_select is not used */
+  int32_t *table;  /* [batch][table_width] */
+  int32_t *lens;   /* [batch] tokens each request holds, 0..table_width * page_size */
+  int batch;       /* 1..max_batch */
+} rtvla_paged_kv;
+
+/* Creates a context: checks the shape, builds the RoPE tables (angles in fp64), allocates the
+ * workspaces.  Synchronous.  Errors: INVALID_ARG, UNSUPPORTED (head_dim, head group, dtype,
+ * page_size), OOM, CUDA.  Reads RTVLA_CHECKED and RTVLA_DEVICE_MEMORY_CAP as rtvla_create does. */
+rtvla_status rtvla_pages_create(const rtvla_pages_config *cfg, rtvla_pages_ctx **out);
+
+/*
+ * Block tables, slots and positions of a step, from request lengths.
+ *   lens   device int32 [batch]: tokens each request holds before the step
+ *   delta  device int32 [batch]: > 0 adds that many tokens, < 0 drops the last -delta tokens
+ *          (all of them when fewer are held), 0 leaves the request
+ *   free_pages device int32 [n_pages], n_free device int32 [1]: a stack, its top at n_free - 1
+ * Pages that a request no longer needs are pushed in request and page order; then new pages are
+ * popped in request and page order and written to kv->table.  Results:
+ *   kv->lens [batch] the new lengths; kv->table the new pages (other entries are left);
+ *   n_free_out [1]; free_pages (entries below the new top; what is popped stays as it was)
+ *   row_start device int32 [batch + 1]: request b's new tokens are rows row_start[b] ..
+ *   slots, positions device int32 [n_rows]: slot and position of every row; slot -1, position 0
+ *     for rows past the last
+ * kv->lens may be lens, and n_free_out may be n_free (then a captured step replays in place).
+ * kv->k, kv->v and kv->k_mean are not used.  A request whose new pages do not fit in what is free
+ * is refused, and with it every later request that needs pages: it keeps its length, its rows get
+ * slot -1, and rtvla_pages_sync_status reports NO_PAGES.  A length outside its range, tokens past
+ * table_width pages or rows past n_rows refuse that request alone and report DEVICE_BOUNDS; a page
+ * number outside the pool (in the table or the free list) gives its rows slot -1 and reports the
+ * same.  row_start counts every request's rows, refused ones too, up to n_rows.
+ * n_rows 0..2^24; slots and positions may be null when it is 0.  Errors: INVALID_ARG, SHAPE, CUDA.
+ */
+rtvla_status rtvla_pages_plan(rtvla_pages_ctx *ctx, const int32_t *lens, const int32_t *delta,
+                              int32_t *free_pages, const int32_t *n_free, const rtvla_paged_kv *kv,
+                              int32_t *n_free_out, int32_t *slots, int32_t *positions,
+                              int32_t *row_start, int n_rows, void *stream);
+
+/*
+ * Writes one layer's new rows.  qkv: device [n_rows][(n_q_heads + 2 n_kv_heads) * head_dim] of
+ * qkv_dtype (the cache's dtype or F32): per row the query heads, then K, then V.  Q and K are
+ * rotated by positions[row], rounded once to the cache's dtype; K and V go to slots[row], Q to
+ * q_out, device [n_rows][n_q_heads * head_dim].  Rows with slot -1 are skipped: nothing of theirs
+ * is written.  A row whose token is the last of its page also writes that page's k_mean (when not
+ * null): the mean, summed in fp32, of the page's keys as stored.  A page's earlier tokens must be
+ * in the pool already or in this call's rows directly before; slots must be distinct.  Reads
+ * kv->k, v, k_mean only.  A slot or position outside the cache skips its row and reports
+ * DEVICE_BOUNDS.  Errors: INVALID_ARG (null, misaligned, n_rows < 0), SHAPE, CUDA.
+ */
+rtvla_status rtvla_pages_write(rtvla_pages_ctx *ctx, int layer, const void *qkv, int qkv_dtype,
+                               const int32_t *slots, const int32_t *positions, int n_rows,
+                               const rtvla_paged_kv *kv, void *q_out, void *stream);
+
+/*
+ * Attention of one query token per request: out[b][h] = sum_j softmax_j(q[b][h] . k_j /
+ * sqrt(head_dim)) v_j over the kv->lens[b] keys request b holds (its own, if written before); 0
+ * where it holds none.  q, out: device [batch][n_q_heads][head_dim] of the cache's dtype, 16-byte
+ * aligned.  sel, if not null: device int32 [batch][n_kv_heads][sel_width], the logical pages
+ * (0 .. pages held - 1) to attend to instead of all, the first min(sel_width, pages held) entries
+ * used; a page listed twice counts twice.  Sums, maxima and weights are fp32.  A length past the
+ * table is clamped; keys of a page number outside the pool, or of a listed page that is not held,
+ * are left out; each reports DEVICE_BOUNDS.  Errors: INVALID_ARG, SHAPE, CUDA.
+ */
+rtvla_status rtvla_pages_attend(rtvla_pages_ctx *ctx, int layer, const void *q, const rtvla_paged_kv *kv,
+                                const int32_t *sel, int sel_width, void *out, void *stream);
+
+/*
+ * Chooses the pages each request's query attends to: sel, device int32 [batch][n_kv_heads][budget],
+ * ascending, -1 past the last.  A request that holds at most `budget` pages gets them all.
+ * Otherwise its first keep_first and its last keep_last pages (the last one need not be full), and
+ * of the others those with the highest score (sum of the KV head's query heads) . k_mean[page],
+ * equal scores by lower page number.  The products are exact and their sum is fp64, so the choice
+ * does not depend on the order of summation short of fp64 rounding.  keep_first >= 0, keep_last >= 1,
+ * keep_first + keep_last <= budget <= 65536.  A page number outside the pool scores below every
+ * other page and reports DEVICE_BOUNDS.  Errors: INVALID_ARG (k_mean null), SHAPE, UNSUPPORTED
+ * (has_select 0), CUDA.
+ */
+rtvla_status rtvla_pages_select(rtvla_pages_ctx *ctx, int layer, const void *q, const rtvla_paged_kv *kv,
+                                int budget, int keep_first, int keep_last, int32_t *sel, void *stream);
+
+/* As rtvla_sync_status, for a paged-cache context (NO_PAGES, DEVICE_BOUNDS, GUARD_OVERWRITE). */
+rtvla_status rtvla_pages_sync_status(rtvla_pages_ctx *ctx, void *stream);
+
+/* Frees everything the context owns (waits for the device first).  NULL is a no-op. */
+void rtvla_pages_destroy(rtvla_pages_ctx *ctx);
 
 #ifdef __cplusplus
 }

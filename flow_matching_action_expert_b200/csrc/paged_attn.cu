@@ -1,4 +1,24 @@
 // Attention of one query token per request over its pages: out = softmax(q K^T / sqrt(d)) V.
+//
+// Every key and value is read once and used by the G = n_q_heads / n_kv_heads heads that share
+// it, 4 G d flops per 4 d bytes: far below the tensor cores' 250 flops per byte, so the kernel is
+// built to keep HBM busy, and the products run on mma.sync m16n8k16 tiles because those take the
+// G heads as the narrow side (N = 8): S^T = K Q^T with 16 keys as M, O^T = V^T P^T with 16
+// components of d as M.  (A tcgen05 tile has M >= 64 and its operands in one shared buffer per
+// CTA; with 8 query rows it would only add barriers.)
+//
+// One warp owns a 16-key tile and a private ring of stages filled by cp.async, so that nothing in
+// the main loop waits for another warp; each warp keeps its own running maximum, sum and O^T in
+// registers.  At the end of a request's keys the four warps' results are joined in shared memory.
+//
+// The work is split evenly whatever the lengths: the 64-key chunks of all (request, KV head)
+// pairs, in order, are cut into one contiguous range per CTA.  A pair that lies inside one range is
+// finished there; of one that is cut each part goes to a workspace in fp32 and k_pages_join adds
+// the parts.  Both kernels find their place by summing the lengths themselves, so no plan has to
+// be made on the host and a captured graph stays valid when the lengths change.
+//
+// Weights are split into two 16-bit halves, p = hi + lo, and multiplied twice: the products cost
+// nothing next to the loads, and the weights then count to 2^-16 instead of 2^-8.
 #include <cuda_fp16.h>
 
 #include "pages.h"
@@ -7,78 +27,531 @@
 namespace rtvla {
 
 namespace {
-__device__ __forceinline__ float to_f(bf16 v) { return __bfloat162float(v); }
-__device__ __forceinline__ float to_f(__half v) { return __half2float(v); }
+
+constexpr int WARPS = 4;
+constexpr int CHUNK = 64;  // keys per unit of work: one 16-key tile per warp
+constexpr int STAGES = 3;
+
 __device__ __forceinline__ void put(bf16 *p, float v) { *p = __float2bfloat16_rn(v); }
 __device__ __forceinline__ void put(__half *p, float v) { *p = __float2half_rn(v); }
+
+// two values as (first in the low half) 16-bit hi parts and the 16-bit rest
+__device__ __forceinline__ void split2(float a, float b, uint32_t &hi, uint32_t &lo, bf16) {
+  const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
+  const __nv_bfloat162 l = __floats2bfloat162_rn(a - __low2float(h), b - __high2float(h));
+  hi = *reinterpret_cast<const uint32_t *>(&h);
+  lo = *reinterpret_cast<const uint32_t *>(&l);
+}
+__device__ __forceinline__ void split2(float a, float b, uint32_t &hi, uint32_t &lo, __half) {
+  const __half2 h = __floats2half2_rn(a, b);
+  const __half2 l = __floats2half2_rn(a - __low2float(h), b - __high2float(h));
+  hi = *reinterpret_cast<const uint32_t *>(&h);
+  lo = *reinterpret_cast<const uint32_t *>(&l);
+}
+
+__device__ __forceinline__ void mma(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1, bf16) {
+  mma_16816(c, a[0], a[1], a[2], a[3], b0, b1);
+}
+__device__ __forceinline__ void mma(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1, __half) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
+      "{%0,%1,%2,%3};"
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+// transposes an 8 x 8 tile of 16-bit values spread over the warp as an mma accumulator row pair
+__device__ __forceinline__ uint32_t transpose8(uint32_t v) {
+  uint32_t r;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(v));
+  return r;
+}
+
+// 16 bytes global -> shared, zeros when !take (nothing is read then)
+__device__ __forceinline__ void copy16(uint32_t dst, const void *src, bool take) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(take ? 16 : 0) : "memory");
+}
+__device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void copy_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
+// chunks of request b (of each of its KV heads)
+__device__ __forceinline__ int chunks_of(const PagedAttnParams &p, int b) {
+  bool bad = false;
+  const int len = pg_len(p.lens[b], p.g, &bad);
+  return (pg_list_len(len, p.sel_width, p.sel != nullptr, p.g) + CHUNK - 1) / CHUNK;
+}
+
+// byte offset of 16-byte chunk c of row r in a tile of D-wide 16-bit rows: chunks are XORed with
+// the row so that the 8 rows of an ldmatrix fall on different banks
+template <int D>
+__device__ __forceinline__ uint32_t tile_at(int r, int c) {
+  return (uint32_t)(r * D * 2 + ((c ^ (r & 7)) << 4));
+}
+
+template <int D, int NT>
+struct Smem {
+  static constexpr int TILE = 16 * D * 2;                 // bytes of 16 rows
+  static constexpr int RING = STAGES * 2 * TILE;          // one warp's K and V stages
+  static constexpr int Q = NT * 8 * D * 2;
+  static constexpr int OLD = D + 4;                       // floats per head of a warp's result
+  static constexpr int TOTAL = WARPS * RING + Q;
+  static_assert(NT * 8 * OLD * 4 <= RING, "a warp's result fits its ring");
+};
+
 }  // namespace
 
-// One CTA per request and query head; a warp takes every fourth key, with its own running
-// maximum, sum and output, joined at the end.
-template <typename T, int D>
-__global__ void __launch_bounds__(128) k_pages_attend(PagedAttnParams p) {
-  constexpr int E = D / 32;
+// NT: query heads in tiles of 8 (1: G <= 8, 2: G <= 16)
+template <typename T, int D, int NT>
+__global__ void __launch_bounds__(WARPS * 32) k_pages_attend(PagedAttnParams p) {
+  using S = Smem<D, NT>;
+  extern __shared__ __align__(128) uint8_t smem[];
+  __shared__ long long warp_sum_s[WARPS];
+  __shared__ long long first_at;
+  __shared__ int first_b;
+  __shared__ uint32_t live_s[WARPS][STAGES];
+  __shared__ float2 ml_s[WARPS][NT * 8];
   const PageGeom g = p.g;
-  const int hq = blockIdx.x, b = blockIdx.y, h = hq / (p.n_q_heads / g.n_kv_heads);
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, gq = lane >> 2, t4 = lane & 3;
+  const int G = p.n_q_heads / g.n_kv_heads, B = p.batch;
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+
+  // this CTA's range of chunks, and the request it starts in
+  const int per = (B + WARPS * 32 - 1) / (WARPS * 32);
+  const int b0 = min(B, (int)threadIdx.x * per), b1 = min(B, b0 + per);
+  long long mine = 0;
   bool bad = false;
-  const int len = pg_len(p.lens[b], g, &bad);
-  const int n = pg_list_len(len, p.sel_width, p.sel != nullptr, g);
-  const int32_t *sel = p.sel ? p.sel + ((size_t)b * g.n_kv_heads + h) * p.sel_width : nullptr;
-  const size_t q0 = ((size_t)b * p.n_q_heads + hq) * D;
-  float q[E], o[E], m = -INFINITY, l = 0.f;
-#pragma unroll
-  for (int i = 0; i < E; ++i) {
-    q[i] = to_f(static_cast<const T *>(p.q)[q0 + lane + 32 * i]) * p.scale_log2;
-    o[i] = 0.f;
-  }
-  for (int j = warp; j < n; j += 4) {
-    const int row = pg_key_row(p.table + (size_t)b * g.width, sel, j, n, len, g, &bad);
-    if (row < 0) continue;
-    const size_t at = pg_elem(p.layer, row, h, g) + lane;
-    float s = 0.f;
-#pragma unroll
-    for (int i = 0; i < E; ++i) s += q[i] * to_f(static_cast<const T *>(p.k)[at + 32 * i]);
-    s = warp_sum(s);
-    const float nm = fmaxf(m, s), ref = nm == -INFINITY ? 0.f : nm;
-    const float a = exp2f(m - ref), w = exp2f(s - ref);
-    m = nm;
-    l = l * a + w;
-#pragma unroll
-    for (int i = 0; i < E; ++i) o[i] = o[i] * a + w * to_f(static_cast<const T *>(p.v)[at + 32 * i]);
-  }
-  __shared__ float so[4][D], sm[4], sl[4];
-#pragma unroll
-  for (int i = 0; i < E; ++i) so[warp][lane + 32 * i] = o[i];
-  if (lane == 0) {
-    sm[warp] = m;
-    sl[warp] = l;
+  for (int b = b0; b < b1; ++b) {
+    mine += chunks_of(p, b);
+    if (blockIdx.x == 0) pg_len(p.lens[b], g, &bad);
   }
   if (bad) set_error(p.ctl, DEVERR_BOUNDS, PG_AT_ATTEND);
-  __syncthreads();
-  const float M = fmaxf(fmaxf(sm[0], sm[1]), fmaxf(sm[2], sm[3])), ref = M == -INFINITY ? 0.f : M;
-  float L = 0.f;
-  for (int w = 0; w < 4; ++w) L += sl[w] * exp2f(sm[w] - ref);
-  for (int i = threadIdx.x; i < D; i += 128) {
-    float v = 0.f;
-    for (int w = 0; w < 4; ++w) v += so[w][i] * exp2f(sm[w] - ref);
-    put(static_cast<T *>(p.out) + q0 + i, L > 0.f ? v / L : 0.f);
+  if (threadIdx.x == 0) {
+    first_b = 0;
+    first_at = 0;
   }
+  long long inc = mine;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const long long n = __shfl_up_sync(0xffffffffu, inc, o);
+    if (lane >= o) inc += n;
+  }
+  if (lane == 31) warp_sum_s[warp] = inc;
+  __syncthreads();
+  long long before = inc - mine, total = 0;
+#pragma unroll
+  for (int w = 0; w < WARPS; ++w) {
+    if (w < warp) before += warp_sum_s[w];
+    total += warp_sum_s[w];
+  }
+  total *= g.n_kv_heads;
+  before *= g.n_kv_heads;
+  const long long ctas = min(total, (long long)gridDim.x);  // those with work: every range holds a chunk
+  if (blockIdx.x >= ctas) return;
+  const long long start = total * blockIdx.x / ctas, end = total * (blockIdx.x + 1) / ctas;
+  if (before <= start && start < before + mine * g.n_kv_heads) {
+    int b = b0;
+    for (; b < b1 - 1; ++b) {
+      const long long n = (long long)chunks_of(p, b) * g.n_kv_heads;
+      if (start < before + n) break;
+      before += n;
+    }
+    first_b = b;
+    first_at = start - before;
+  }
+  __syncthreads();
+  int b = first_b, n_chunks = max(chunks_of(p, b), 1);
+  int h = min((int)(first_at / n_chunks), g.n_kv_heads - 1), c0 = (int)(first_at % n_chunks);
+  long long left = end - start;
+  bool at_start = true;
+
+  uint8_t *ring = smem + warp * S::RING;
+  const uint32_t ring_a = smem_u32(ring), q_a = smem_u32(smem + WARPS * S::RING);
+  const T *kp = static_cast<const T *>(p.k), *vp = static_cast<const T *>(p.v);
+
+  while (true) {
+    // ---- one segment: chunks [c0, c1) of (b, h)
+    const int c1 = (int)min((long long)n_chunks, c0 + left);
+    const int len = pg_len(p.lens[b], g, &bad);
+    const int n = pg_list_len(len, p.sel_width, p.sel != nullptr, g);
+    const int32_t *trow = p.table + (size_t)b * g.width;
+    const int32_t *sel = p.sel ? p.sel + ((size_t)b * g.n_kv_heads + h) * p.sel_width : nullptr;
+    const int tiles_end = min(c1 * 4, (n + 15) >> 4);
+
+    // row of the cache (all layers, pages and heads counted together) of key j, or ~0
+    auto row_of = [&](int j) -> uint32_t {
+      const int r = pg_key_row(trow, sel, j, n, len, g, &bad);
+      if (r < 0) return ~0u;
+      return (uint32_t)(((((size_t)p.layer * g.n_pages + (r >> g.shift)) * g.n_kv_heads + h) << g.shift) +
+                        (r & ((1 << g.shift) - 1)));
+    };
+    auto load = [&](int stage, uint32_t row) {  // lanes 0..15 hold the tile's rows
+      constexpr int CPR = D / 8, RPI = 32 / CPR;  // 16-byte chunks per row, rows per instruction
+      const uint32_t base = ring_a + stage * 2 * S::TILE;
+      const int c = lane % CPR;
+#pragma unroll
+      for (int i = 0; i < 16 / RPI; ++i) {
+        const int r = i * RPI + lane / CPR;
+        const uint32_t at = __shfl_sync(0xffffffffu, row, r);
+        const bool take = at != ~0u;
+        const size_t off = (take ? (size_t)at * D : 0) + c * 8;
+        copy16(base + tile_at<D>(r, c), kp + off, take);
+        copy16(base + S::TILE + tile_at<D>(r, c), vp + off, take);
+      }
+      const uint32_t live = __ballot_sync(0xffffffffu, row != ~0u);
+      if (lane == 0) live_s[warp][stage] = live;
+    };
+
+    int tile = c0 * 4 + warp;
+    uint32_t row = lane < 16 ? row_of(tile * 16 + lane) : ~0u;
+#pragma unroll
+    for (int s = 0; s < STAGES - 1; ++s) {
+      const int next = tile + s * WARPS;
+      if (next < tiles_end) {
+        load(s, row);
+        row = lane < 16 ? row_of((next + WARPS) * 16 + lane) : ~0u;
+      }
+      copy_commit();
+    }
+    // the group's query heads, zero rows past G
+    {
+      const T *q = static_cast<const T *>(p.q) + ((size_t)b * p.n_q_heads + h * G) * D;
+      for (int i = threadIdx.x; i < NT * 8 * (D / 8); i += WARPS * 32) {
+        const int r = i / (D / 8), c = i % (D / 8);
+        const uint4 v = r < G ? *reinterpret_cast<const uint4 *>(q + (size_t)r * D + c * 8) : make_uint4(0, 0, 0, 0);
+        *reinterpret_cast<uint4 *>(smem + WARPS * S::RING + tile_at<D>(r, c)) = v;
+      }
+    }
+    __syncthreads();
+
+    float o[D / 16][NT][4], m[NT][2], l[NT][2];
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+      m[nt][0] = m[nt][1] = -INFINITY;
+      l[nt][0] = l[nt][1] = 0.f;
+#pragma unroll
+      for (int i = 0; i < D / 16; ++i) o[i][nt][0] = o[i][nt][1] = o[i][nt][2] = o[i][nt][3] = 0.f;
+    }
+
+    int stage = 0;
+#pragma unroll 1
+    for (; tile < tiles_end; tile += WARPS) {
+      copy_wait<STAGES - 2>();
+      __syncwarp();
+      const uint32_t live = live_s[warp][stage];
+      {
+        const int next = tile + (STAGES - 1) * WARPS;
+        if (next < tiles_end) {
+          load(stage == 0 ? STAGES - 1 : stage - 1, row);
+          row = lane < 16 ? row_of((next + WARPS) * 16 + lane) : ~0u;
+        }
+        copy_commit();
+      }
+      const uint32_t ka = ring_a + stage * 2 * S::TILE, va = ka + S::TILE;
+
+      // S^T = K Q^T: rows (keys) gq and gq + 8, columns (heads) 2 t4 and 2 t4 + 1
+      float s[NT][2][4];
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) s[nt][0][e] = s[nt][1][e] = 0.f;
+#pragma unroll
+      for (int kk = 0; kk < D / 16; kk += 2) {
+        uint32_t a[2][4];
+#pragma unroll
+        for (int u = 0; u < 2; ++u)
+          ldsm_x4(a[u][0], a[u][1], a[u][2], a[u][3],
+                  ka + tile_at<D>((lane & 7) + ((lane >> 3) & 1) * 8, 2 * (kk + u) + (lane >> 4)));
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+          uint32_t q0, q1, q2, q3;
+          ldsm_x4(q0, q1, q2, q3, q_a + tile_at<D>(nt * 8 + (lane & 7), 2 * kk + (lane >> 3)));
+          mma(s[nt][0], a[0], q0, q1, T());
+          mma(s[nt][1], a[1], q2, q3, T());
+        }
+      }
+      uint32_t hi[NT][2], lo[NT][2];
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt) {
+        float x[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          x[e] = (live >> (gq + (e >> 1) * 8)) & 1 ? (s[nt][0][e] + s[nt][1][e]) * p.scale_log2 : -INFINITY;
+        float a[2];
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          float cm = fmaxf(x[e], x[e + 2]);
+#pragma unroll
+          for (int w = 4; w < 32; w <<= 1) cm = fmaxf(cm, __shfl_xor_sync(0xffffffffu, cm, w));
+          const float nm = fmaxf(m[nt][e], cm), ref = nm == -INFINITY ? 0.f : nm;
+          a[e] = exp2f(m[nt][e] - ref);
+          m[nt][e] = nm;
+          x[e] = exp2f(x[e] - ref);
+          x[e + 2] = exp2f(x[e + 2] - ref);
+          l[nt][e] = l[nt][e] * a[e] + (x[e] + x[e + 2]);
+        }
+        if (__any_sync(0xffffffffu, a[0] != 1.f || a[1] != 1.f)) {
+#pragma unroll
+          for (int i = 0; i < D / 16; ++i) {
+            o[i][nt][0] *= a[0];
+            o[i][nt][1] *= a[1];
+            o[i][nt][2] *= a[0];
+            o[i][nt][3] *= a[1];
+          }
+        }
+        split2(x[0], x[1], hi[nt][0], lo[nt][0], T());
+        split2(x[2], x[3], hi[nt][1], lo[nt][1], T());
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          hi[nt][e] = transpose8(hi[nt][e]);
+          lo[nt][e] = transpose8(lo[nt][e]);
+        }
+      }
+      // O^T += V^T P^T: rows (components) 16 i + gq and + 8, columns (heads) 2 t4 and 2 t4 + 1
+#pragma unroll
+      for (int i = 0; i < D / 16; ++i) {
+        uint32_t a[4];
+        ldsm_x4_t(a[0], a[1], a[2], a[3],
+                  va + tile_at<D>((lane & 7) + (lane >> 4) * 8, 2 * i + ((lane >> 3) & 1)));
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+          mma(o[i][nt], a, hi[nt][0], hi[nt][1], T());
+          mma(o[i][nt], a, lo[nt][0], lo[nt][1], T());
+        }
+      }
+      stage = stage == STAGES - 1 ? 0 : stage + 1;
+      __syncwarp();
+    }
+
+    // ---- join the warps: each puts its result into its own ring
+    float *so = reinterpret_cast<float *>(ring);
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        float sum = l[nt][e];
+#pragma unroll
+        for (int w = 4; w < 32; w <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, w);
+        const int head = nt * 8 + 2 * t4 + e;
+        if (gq == 0) ml_s[warp][head] = make_float2(m[nt][e], sum);
+#pragma unroll
+        for (int i = 0; i < D / 16; ++i) {
+          so[head * S::OLD + 16 * i + gq] = o[i][nt][e];
+          so[head * S::OLD + 16 * i + gq + 8] = o[i][nt][e + 2];
+        }
+      }
+    __syncthreads();
+    const bool whole = c0 == 0 && c1 == n_chunks;
+    const size_t part = (size_t)blockIdx.x * 2 + (at_start ? 0 : 1);
+    for (int i = threadIdx.x; i < G * (D / 4); i += WARPS * 32) {
+      const int head = i / (D / 4), d = (i % (D / 4)) * 4;
+      float M = -INFINITY, L = 0.f;
+#pragma unroll
+      for (int w = 0; w < WARPS; ++w) M = fmaxf(M, ml_s[w][head].x);
+      const float ref = M == -INFINITY ? 0.f : M;
+      float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+      for (int w = 0; w < WARPS; ++w) {
+        const float f = exp2f(ml_s[w][head].x - ref);
+        const float4 x = *reinterpret_cast<const float4 *>(reinterpret_cast<float *>(smem + w * S::RING) +
+                                                           head * S::OLD + d);
+        L += f * ml_s[w][head].y;
+        v.x += f * x.x;
+        v.y += f * x.y;
+        v.z += f * x.z;
+        v.w += f * x.w;
+      }
+      if (whole) {
+        const float inv = L > 0.f ? 1.f / L : 0.f;
+        T *out = static_cast<T *>(p.out) + ((size_t)b * p.n_q_heads + h * G + head) * D + d;
+        put(out, v.x * inv);
+        put(out + 1, v.y * inv);
+        put(out + 2, v.z * inv);
+        put(out + 3, v.w * inv);
+      } else {
+        *reinterpret_cast<float4 *>(p.part_o + (part * G + head) * D + d) = v;
+        if (d == 0) p.part_ml[part * G + head] = make_float2(M, L);
+      }
+    }
+
+    left -= c1 - c0;
+    if (left == 0) break;
+    __syncthreads();
+    at_start = false;
+    c0 = 0;
+    if (++h == g.n_kv_heads) {  // the next request that holds anything
+      h = 0;
+      for (++b; b < B; b += 32) {
+        const int c = b + lane < B ? chunks_of(p, b + lane) : 0;
+        const unsigned some = __ballot_sync(0xffffffffu, c > 0);
+        if (some) {
+          const int at = __ffs(some) - 1;
+          n_chunks = __shfl_sync(0xffffffffu, c, at);
+          b += at;
+          break;
+        }
+      }
+      if (b >= B) break;  // only if the lengths changed under the kernel
+    }
+  }
+  if (bad) set_error(p.ctl, DEVERR_BOUNDS, PG_AT_ATTEND);
+}
+
+// Adds the parts of one (request, query head) that was cut across CTAs of k_pages_attend, and
+// writes the zeros of a request that holds nothing.  256 threads: D / 4 columns, the rest share
+// the parts.  Launched before the parts are complete; it finds its place meanwhile.
+template <typename T, int D>
+__global__ void __launch_bounds__(256) k_pages_join(PagedAttnParams p, int grid) {
+  constexpr int COLS = D / 4, ROWS = 256 / COLS;
+  __shared__ long long sum_s[2][8];
+  __shared__ float4 acc_s[ROWS][COLS];
+  __shared__ float2 ml_s[ROWS];
+  const PageGeom g = p.g;
+  const int hq = blockIdx.x, b = blockIdx.y, G = p.n_q_heads / g.n_kv_heads, h = hq / G;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  long long before = 0, total = 0;
+  for (int i = threadIdx.x; i < p.batch; i += 256) {
+    const long long c = chunks_of(p, i);
+    total += c;
+    if (i < b) before += c;
+  }
+#pragma unroll
+  for (int w = 16; w > 0; w >>= 1) {
+    before += __shfl_xor_sync(0xffffffffu, before, w);
+    total += __shfl_xor_sync(0xffffffffu, total, w);
+  }
+  if (lane == 0) {
+    sum_s[0][warp] = before;
+    sum_s[1][warp] = total;
+  }
+  __syncthreads();
+  before = total = 0;
+#pragma unroll
+  for (int w = 0; w < 8; ++w) {
+    before += sum_s[0][w];
+    total += sum_s[1][w];
+  }
+  const long long n = chunks_of(p, b);
+  T *out = static_cast<T *>(p.out) + ((size_t)b * p.n_q_heads + hq) * D;
+  total *= g.n_kv_heads;
+  const long long x0 = before * g.n_kv_heads + n * h, x1 = x0 + n;
+  const long long ctas = max(min(total, (long long)grid), 1ll);
+  // chunk x belongs to the CTA c with total c / ctas <= x < total (c + 1) / ctas
+  const int from = n ? (int)(((x0 + 1) * ctas - 1) / total) : 0, to = n ? (int)((x1 * ctas - 1) / total) : 0;
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  if (n == 0) {
+    for (int i = threadIdx.x; i < D; i += 256) put(out + i, 0.f);
+    return;
+  }
+  if (from == to) return;  // finished where it was computed
+  const int col = threadIdx.x % COLS, row = threadIdx.x / COLS, head = hq - h * G;
+  float M = -INFINITY, L = 0.f;
+  float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+  for (int c = from + row; c <= to; c += ROWS) {
+    const size_t at = ((size_t)c * 2 + (total * c / ctas < x0 ? 1 : 0)) * G + head;
+    const float2 ml = p.part_ml[at];
+    const float4 x = *reinterpret_cast<const float4 *>(p.part_o + at * D + col * 4);
+    const float nm = fmaxf(M, ml.x), ref = nm == -INFINITY ? 0.f : nm;
+    const float a = exp2f(M - ref), f = exp2f(ml.x - ref);
+    M = nm;
+    L = L * a + f * ml.y;
+    v.x = v.x * a + f * x.x;
+    v.y = v.y * a + f * x.y;
+    v.z = v.z * a + f * x.z;
+    v.w = v.w * a + f * x.w;
+  }
+  acc_s[row][col] = v;
+  if (col == 0) ml_s[row] = make_float2(M, L);
+  __syncthreads();
+  if (row != 0) return;
+  M = -INFINITY;
+  for (int r = 0; r < ROWS; ++r) M = fmaxf(M, ml_s[r].x);
+  const float ref = M == -INFINITY ? 0.f : M;
+  L = 0.f;
+  v = make_float4(0.f, 0.f, 0.f, 0.f);
+  for (int r = 0; r < ROWS; ++r) {
+    const float f = exp2f(ml_s[r].x - ref);
+    const float4 x = acc_s[r][col];
+    L += f * ml_s[r].y;
+    v.x += f * x.x;
+    v.y += f * x.y;
+    v.z += f * x.z;
+    v.w += f * x.w;
+  }
+  const float inv = L > 0.f ? 1.f / L : 0.f;
+  put(out + col * 4, v.x * inv);
+  put(out + col * 4 + 1, v.y * inv);
+  put(out + col * 4 + 2, v.z * inv);
+  put(out + col * 4 + 3, v.w * inv);
 }
 
 namespace {
-template <typename T>
-cudaError_t attend(const PagedAttnParams &p, cudaStream_t st) {
-  const dim3 grid(p.n_q_heads, p.batch);
-  if (p.g.head_dim == 64) k_pages_attend<T, 64><<<grid, 128, 0, st>>>(p);
-  else if (p.g.head_dim == 128) k_pages_attend<T, 128><<<grid, 128, 0, st>>>(p);
-  else k_pages_attend<T, 256><<<grid, 128, 0, st>>>(p);
-  return cudaGetLastError();
+
+// CTAs that fit on an SM by shared memory (227 KB, 1 KB of it per CTA reserved)
+template <int D, int NT>
+constexpr int ctas_per_sm() {
+  return (227 * 1024) / (Smem<D, NT>::TOTAL + 2048) < 4 ? (227 * 1024) / (Smem<D, NT>::TOTAL + 2048) : 4;
 }
+
+template <typename T, int D, int NT>
+cudaError_t attend(const PagedAttnParams &p, int sm_count, cudaStream_t st) {
+  // one wave of CTAs, but no more than there can be chunks
+  const long long keys = (long long)(p.sel && p.sel_width < p.g.width ? p.sel_width : p.g.width) << p.g.shift;
+  const long long most = (long long)p.batch * p.g.n_kv_heads * ((keys + CHUNK - 1) / CHUNK);
+  const long long wave = (long long)sm_count * ctas_per_sm<D, NT>();
+  const int ctas = (int)(most < wave ? most : wave);
+  k_pages_attend<T, D, NT><<<ctas, WARPS * 32, Smem<D, NT>::TOTAL, st>>>(p);
+  const cudaError_t e = cudaGetLastError();
+  if (e != cudaSuccess) return e;
+  cudaLaunchAttribute attr;
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(p.n_q_heads, p.batch);
+  cfg.blockDim = dim3(256);
+  cfg.stream = st;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, k_pages_join<T, D>, p, ctas);
+}
+
+template <typename T, int D>
+cudaError_t attend(const PagedAttnParams &p, int sm_count, cudaStream_t st) {
+  return p.n_q_heads / p.g.n_kv_heads <= 8 ? attend<T, D, 1>(p, sm_count, st) : attend<T, D, 2>(p, sm_count, st);
+}
+
+template <typename T>
+cudaError_t attend(const PagedAttnParams &p, int sm_count, cudaStream_t st) {
+  if (p.g.head_dim == 64) return attend<T, 64>(p, sm_count, st);
+  return p.g.head_dim == 128 ? attend<T, 128>(p, sm_count, st) : attend<T, 256>(p, sm_count, st);
+}
+
+template <typename T, int D>
+cudaError_t allow_smem() {
+  const cudaError_t e = cudaFuncSetAttribute(k_pages_attend<T, D, 1>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                             Smem<D, 1>::TOTAL);
+  return e != cudaSuccess ? e
+                          : cudaFuncSetAttribute(k_pages_attend<T, D, 2>,
+                                                 cudaFuncAttributeMaxDynamicSharedMemorySize, Smem<D, 2>::TOTAL);
+}
+
 }  // namespace
 
-cudaError_t launch_pages_attend(const PagedAttnParams &p, int dtype, cudaStream_t st) {
-  return dtype == RTVLA_DTYPE_BF16 ? attend<bf16>(p, st) : attend<__half>(p, st);
+int pages_attend_parts(int sm_count) { return 2 * 4 * sm_count; }
+
+cudaError_t pages_attend_init_attributes() {
+  cudaError_t e = allow_smem<bf16, 64>();
+  if (e == cudaSuccess) e = allow_smem<bf16, 128>();
+  if (e == cudaSuccess) e = allow_smem<bf16, 256>();
+  if (e == cudaSuccess) e = allow_smem<__half, 64>();
+  if (e == cudaSuccess) e = allow_smem<__half, 128>();
+  if (e == cudaSuccess) e = allow_smem<__half, 256>();
+  return e;
+}
+
+cudaError_t launch_pages_attend(const PagedAttnParams &p, int dtype, int sm_count, cudaStream_t st) {
+  return dtype == RTVLA_DTYPE_BF16 ? attend<bf16>(p, sm_count, st) : attend<__half>(p, sm_count, st);
 }
 
 }  // namespace rtvla

@@ -57,9 +57,13 @@ struct PagedAttnParams {
   int sel_width;
   void *out;              // [batch][n_q_heads][head_dim]
   float scale_log2;       // log2(e) / sqrt(head_dim)
+  float *part_o;          // workspace [parts][group][head_dim]: unnormalised parts of cut requests
+  float2 *part_ml;        // workspace [parts][group]: their maximum (log2 units) and sum
   DevCtl *ctl;
 };
-cudaError_t launch_pages_attend(const PagedAttnParams &p, int dtype, cudaStream_t st);
+int pages_attend_parts(int sm_count);  // parts the workspace holds
+cudaError_t pages_attend_init_attributes();
+cudaError_t launch_pages_attend(const PagedAttnParams &p, int dtype, int sm_count, cudaStream_t st);
 
 struct SelectParams {
   PageGeom g;

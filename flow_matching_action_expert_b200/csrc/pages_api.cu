@@ -23,6 +23,8 @@ struct rtvla_pages_ctx {
   GuardRegion *d_guards = nullptr;
   DevCtl *ctl = nullptr;
   float2 *rope_lo = nullptr, *rope_hi = nullptr;
+  float *part_o = nullptr;
+  float2 *part_ml = nullptr;
   unsigned long long *keys = nullptr;  // select: [max_batch][n_kv_heads][table_width]
 };
 
@@ -78,6 +80,8 @@ rtvla_status check_cfg(const rtvla_pages_config *g) {
     return RTVLA_ERR_INVALID_ARG;
   if ((long long)g->n_pages * g->page_size >= (1ll << 31) || (long long)g->table_width * g->page_size > (1ll << 24))
     return RTVLA_ERR_INVALID_ARG;
+  // a row of the cache (layer, page, head, token) is numbered in 32 bits; more would not fit a GPU
+  if ((double)g->n_layers * g->n_pages * g->n_kv_heads * g->page_size >= 4294967295.0) return RTVLA_ERR_INVALID_ARG;
   if (g->n_q_heads % g->n_kv_heads) return RTVLA_ERR_INVALID_ARG;
   if (g->dtype != RTVLA_DTYPE_BF16 && g->dtype != RTVLA_DTYPE_F16) return RTVLA_ERR_UNSUPPORTED;
   if (g->head_dim != 64 && g->head_dim != 128 && g->head_dim != 256) return RTVLA_ERR_UNSUPPORTED;
@@ -89,9 +93,11 @@ rtvla_status check_cfg(const rtvla_pages_config *g) {
 // (cos, sin) of positions step * i, angle = position * theta^(-2j/d) in fp64, rounded once
 rtvla_status build_rope(float2 *dst, int rows, int step, int d, double theta) {
   std::vector<float2> t((size_t)rows * (d / 2));
+  std::vector<double> freq(d / 2);
+  for (int j = 0; j < d / 2; ++j) freq[j] = std::pow(theta, -2.0 * j / d);
   for (int i = 0; i < rows; ++i)
     for (int j = 0; j < d / 2; ++j) {
-      const double a = (double)i * step * std::pow(theta, -2.0 * j / d);
+      const double a = (double)i * step * freq[j];
       t[(size_t)i * (d / 2) + j] = make_float2((float)std::cos(a), (float)std::sin(a));
     }
   return cudaMemcpy(dst, t.data(), t.size() * sizeof(float2), cudaMemcpyHostToDevice) == cudaSuccess
@@ -104,7 +110,7 @@ rtvla_status p_create(rtvla_pages_ctx *c) {
   if (cudaGetDevice(&c->device) != cudaSuccess ||
       cudaDeviceGetAttribute(&c->sm_count, cudaDevAttrMultiProcessorCount, c->device) != cudaSuccess)
     return RTVLA_ERR_CUDA;
-  if (pages_init_attributes() != cudaSuccess) return RTVLA_ERR_CUDA;
+  if (pages_init_attributes() != cudaSuccess || pages_attend_init_attributes() != cudaSuccess) return RTVLA_ERR_CUDA;
   c->ctl = p_alloc<DevCtl>(c, 1);
   if (!c->ctl) return RTVLA_ERR_OOM;
   if (g.rope_theta > 0.f) {
@@ -116,6 +122,10 @@ rtvla_status p_create(rtvla_pages_ctx *c) {
         build_rope(c->rope_hi, hi, 256, g.head_dim, g.rope_theta) != RTVLA_OK)
       return RTVLA_ERR_CUDA;
   }
+  const size_t parts = (size_t)pages_attend_parts(c->sm_count) * (g.n_q_heads / g.n_kv_heads);
+  c->part_o = p_alloc<float>(c, parts * g.head_dim);
+  c->part_ml = p_alloc<float2>(c, parts);
+  if (!c->part_o || !c->part_ml) return RTVLA_ERR_OOM;
   if (g.has_select) {
     c->keys = p_alloc<unsigned long long>(c, (size_t)g.max_batch * g.n_kv_heads * g.table_width);
     if (!c->keys) return RTVLA_ERR_OOM;
@@ -233,9 +243,10 @@ rtvla_status rtvla_pages_attend(rtvla_pages_ctx *c, int layer, const void *q, co
   if (sel && sel_width > 65536) return RTVLA_ERR_SHAPE;
   OnDevice dev(c->device);
   if (!dev.ok) return RTVLA_ERR_CUDA;
-  PagedAttnParams p{c->g,      layer, c->cfg.n_q_heads,   kv->batch, q, kv->k, kv->v, kv->table, kv->lens, sel,
-                    sel_width, out,   (float)(1.4426950408889634 / std::sqrt((double)c->cfg.head_dim)), c->ctl};
-  return launched(launch_pages_attend(p, c->cfg.dtype, static_cast<cudaStream_t>(stream)));
+  const float scale = (float)(1.4426950408889634 / std::sqrt((double)c->cfg.head_dim));
+  PagedAttnParams p{c->g,     layer,    c->cfg.n_q_heads, kv->batch, q,     kv->k,     kv->v,      kv->table,
+                    kv->lens, sel,      sel_width,        out,       scale, c->part_o, c->part_ml, c->ctl};
+  return launched(launch_pages_attend(p, c->cfg.dtype, c->sm_count, static_cast<cudaStream_t>(stream)));
 }
 
 rtvla_status rtvla_pages_select(rtvla_pages_ctx *c, int layer, const void *q, const rtvla_paged_kv *kv, int budget,

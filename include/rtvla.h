@@ -465,7 +465,8 @@ typedef struct {
   int n_kv_heads;   /* 1..64 */
   int head_dim;     /* 64, 128 or 256 */
   int page_size;    /* tokens per page: a power of two, 1..1024 */
-  int n_pages;      /* pages in the pool; n_pages * page_size < 2^31 */
+  int n_pages;      /* pages in the pool; n_pages * page_size < 2^31, n_layers * n_pages * n_kv_heads *
+                       page_size < 2^32 - 1 */
   int table_width;  /* pages one request can hold; table_width * page_size <= 2^24 */
   int max_batch;    /* 1..4096 */
   int has_select;   /* 1: allocate rtvla_pages_select's workspace, 8 bytes per request, KV head and

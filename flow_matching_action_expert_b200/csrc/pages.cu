@@ -271,114 +271,238 @@ __global__ void __launch_bounds__(128) k_pages_write(WriteParams p) {
 // select
 
 namespace {
-// Order-preserving map of a score to an integer; 0 and 1 and the all-ones word are kept free.
+
+constexpr int ST = 512;            // threads of a select CTA
+constexpr int SC = 8;              // CTAs of a cluster: they score, the first one chooses
+constexpr int RUN = 16;            // pages a warp scores at a time
+constexpr int BITS = 11, BINS = 1 << BITS;
+constexpr int SELECT_SMEM_KEYS = 8192;  // keys held in shared memory; longer tables use the workspace
+
+// Order-preserving map of a score to an integer; 0 and 1 are kept for pages outside the pool.
 __device__ __forceinline__ unsigned long long score_key(double s) {
   const unsigned long long u = (unsigned long long)__double_as_longlong(s);
-  const unsigned long long k = (u >> 63) ? ~u : u | 0x8000000000000000ull;
-  return min(max(k, 2ull), ~1ull);
+  return max((u >> 63) ? ~u : u | 0x8000000000000000ull, 2ull);
 }
-constexpr unsigned long long KEY_BAD = 1, KEY_TAKEN = ~0ull;
+constexpr unsigned long long KEY_BAD = 1;
+
+__device__ __forceinline__ void add8(double (&a)[8], const uint4 &v, bf16) {
+  const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    a[2 * i] += (double)__uint_as_float(w[i] << 16);
+    a[2 * i + 1] += (double)__uint_as_float(w[i] & 0xffff0000u);
+  }
+}
+__device__ __forceinline__ void add8(double (&a)[8], const uint4 &v, __half) {
+  const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&w[i]));
+    a[2 * i] += (double)f.x;
+    a[2 * i + 1] += (double)f.y;
+  }
+}
+
+// Exclusive scan of a pair of counts over the block.
+__device__ uint2 scan_pair(uint2 v, uint2 *warp_sums, uint2 *total) {
+  const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
+  uint2 inc = v;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const unsigned x = __shfl_up_sync(0xffffffffu, inc.x, o), y = __shfl_up_sync(0xffffffffu, inc.y, o);
+    if (lane >= o) {
+      inc.x += x;
+      inc.y += y;
+    }
+  }
+  __syncthreads();
+  if (lane == 31) warp_sums[w] = inc;
+  __syncthreads();
+  uint2 before = make_uint2(0, 0), all = make_uint2(0, 0);
+#pragma unroll
+  for (int i = 0; i < ST / 32; ++i) {
+    const uint2 x = warp_sums[i];
+    if (i < w) {
+      before.x += x.x;
+      before.y += x.y;
+    }
+    all.x += x.x;
+    all.y += x.y;
+  }
+  *total = all;
+  return make_uint2(before.x + inc.x - v.x, before.y + inc.y - v.y);
+}
+
 }  // namespace
 
-// One CTA per request and KV head: every page's score, then the best page, budget times over.
-template <typename T>
-__global__ void __launch_bounds__(256) k_pages_select(SelectParams p) {
+// One cluster per request and KV head.  Its CTAs share the scoring (16 bytes of a page's mean per
+// lane, fp64 sums: the means of a long request are a few hundred KB, so this is latency, not
+// bandwidth) and put order-preserving integer keys into the first CTA's shared memory.  That CTA
+// finds the lowest key taken by radix passes from the top bits, which stop as soon as the pages
+// in the deciding bin fit one comparison of all pairs: two passes for ordinary scores.  Selected is
+// then every key above that one, and of the keys equal to it the first few in page order.
+template <typename T, int D>
+__global__ void __cluster_dims__(SC, 1, 1) __launch_bounds__(ST) k_pages_select(SelectParams p) {
+  extern __shared__ unsigned long long smem_keys[];
+  __shared__ int bins[BINS];
+  __shared__ uint2 warp_sums[ST / 32];
+  __shared__ unsigned long long near_key[ST];
+  __shared__ int bin_s, above_s, n_near, near_eq;
+  __shared__ unsigned long long cut_s;
   const PageGeom g = p.g;
-  const int h = blockIdx.x, b = blockIdx.y, d = g.head_dim, G = p.n_q_heads / g.n_kv_heads;
+  const int rank = blockIdx.x, h = blockIdx.y, b = blockIdx.z, G = p.n_q_heads / g.n_kv_heads;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  __shared__ double qs[256];
-  __shared__ unsigned long long best_key[8];
-  __shared__ int best_page[8], counts[8];
   bool bad = false;
   const int held = pg_pages(pg_len(p.lens[b], g, &bad), g);
-  if (bad && threadIdx.x == 0 && h == 0) set_error(p.ctl, DEVERR_BOUNDS, PG_AT_SELECT);
+  if (bad && threadIdx.x == 0 && rank == 0 && h == 0) set_error(p.ctl, DEVERR_BOUNDS, PG_AT_SELECT);
   int *sel = p.sel + ((size_t)b * g.n_kv_heads + h) * p.budget;
-  const int n = min(held, p.budget);
-  if (held <= p.budget) {
-    for (int i = threadIdx.x; i < p.budget; i += 256) sel[i] = i < n ? i : -1;
+  if (held <= p.budget) {  // the whole cluster leaves here
+    for (int i = rank * ST + threadIdx.x; i < p.budget; i += SC * ST) sel[i] = i < held ? i : -1;
     return;
   }
-  const T *q = static_cast<const T *>(p.q) + ((size_t)b * p.n_q_heads + h * G) * d;
-  for (int i = threadIdx.x; i < d; i += 256) {
-    double s = 0.0;
-    for (int j = 0; j < G; ++j) s += (double)to_f(q[j * d + i]);
-    qs[i] = s;
-  }
-  __syncthreads();
-  unsigned long long *keys = p.keys + ((size_t)b * g.n_kv_heads + h) * g.width;
-  const int lo = p.keep_first, hi = held - p.keep_last;
-  for (int e = warp; e < held; e += 8) {
-    unsigned long long key = KEY_TAKEN;
-    if (e >= lo && e < hi) {
-      const int page = pg_page(p.table + (size_t)b * g.width, e, g);
-      if (page < 0) {
-        key = KEY_BAD;
-        if (lane == 0) set_error(p.ctl, DEVERR_BOUNDS, PG_AT_SELECT);
-      } else {
-        const T *m = static_cast<const T *>(p.k_mean) + pg_mean_elem(p.layer, page, h, g);
-        double s = 0.0;
-        for (int i = lane; i < d; i += 32) s += qs[i] * (double)to_f(m[i]);
+  // candidates: logical pages lo .. lo + n - 1, of which `need` are chosen
+  const int lo = p.keep_first, n = held - p.keep_last - lo, need = p.budget - lo - p.keep_last;
+  const bool in_smem = g.width <= SELECT_SMEM_KEYS;
+  unsigned long long *keys = in_smem ? smem_keys : p.keys + ((size_t)b * g.n_kv_heads + h) * g.width;
+  {
+    unsigned long long *dst = keys;
+    if (in_smem) {
+      uint64_t at;
+      asm("mapa.u64 %0, %1, %2;" : "=l"(at) : "l"(reinterpret_cast<uint64_t>(smem_keys)), "r"(0));
+      dst = reinterpret_cast<unsigned long long *>(at);
+    }
+    constexpr int LPP = D / 8, PPW = 32 / LPP;  // lanes per page, pages per load
+    const int sub = lane / LPP, ln = lane % LPP;
+    double qs[8] = {0, 0, 0, 0, 0, 0, 0, 0};
+    const T *q = static_cast<const T *>(p.q) + ((size_t)b * p.n_q_heads + h * G) * D + ln * 8;
+    for (int j = 0; j < G; ++j) add8(qs, *reinterpret_cast<const uint4 *>(q + (size_t)j * D), T());
+    for (int c0 = (rank * (ST / 32) + warp) * RUN; c0 < n; c0 += SC * (ST / 32) * RUN) {
+      const int mine = lane < RUN && c0 + lane < n ? pg_page(p.table + (size_t)b * g.width, lo + c0 + lane, g) : -1;
+      if (lane < RUN && c0 + lane < n && mine < 0) bad = true;
+      constexpr int LOADS = RUN / PPW, AHEAD = LOADS < 8 ? LOADS : 8;
 #pragma unroll
-        for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
-        key = score_key(s);
-      }
-    }
-    if (lane == 0) keys[e] = key;
-  }
-  __syncthreads();
-  for (int left = p.budget - lo - p.keep_last; left > 0; --left) {
-    unsigned long long k = 0;
-    int at = 0;
-    for (int e = lo + threadIdx.x; e < hi; e += 256)
-      if (keys[e] != KEY_TAKEN && keys[e] > k) {
-        k = keys[e];
-        at = e;
-      }
+      for (int i0 = 0; i0 < LOADS; i0 += AHEAD) {
+        uint4 v[AHEAD];
+        int page[AHEAD];
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) {
-      const unsigned long long k2 = __shfl_xor_sync(0xffffffffu, k, o);
-      const int a2 = __shfl_xor_sync(0xffffffffu, at, o);
-      if (k2 > k || (k2 == k && a2 < at)) {
-        k = k2;
-        at = a2;
+        for (int i = 0; i < AHEAD; ++i) {
+          page[i] = __shfl_sync(0xffffffffu, mine, (i0 + i) * PPW + sub);
+          v[i] = make_uint4(0, 0, 0, 0);
+          if (page[i] >= 0)
+            v[i] = *reinterpret_cast<const uint4 *>(static_cast<const T *>(p.k_mean) +
+                                                    pg_mean_elem(p.layer, page[i], h, g) + ln * 8);
+        }
+#pragma unroll
+        for (int i = 0; i < AHEAD; ++i) {
+          double m[8] = {0, 0, 0, 0, 0, 0, 0, 0}, s = 0.0;
+          add8(m, v[i], T());
+#pragma unroll
+          for (int u = 0; u < 8; ++u) s += qs[u] * m[u];
+#pragma unroll
+          for (int o = LPP / 2; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+          const int c = c0 + (i0 + i) * PPW + sub;
+          if (ln == 0 && c < n) dst[c] = page[i] < 0 ? KEY_BAD : score_key(s);
+        }
       }
     }
-    if (lane == 0) {
-      best_key[warp] = k;
-      best_page[warp] = at;
+    if (bad) set_error(p.ctl, DEVERR_BOUNDS, PG_AT_SELECT);
+  }
+  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+  if (rank != 0) return;
+
+  // cut: the lowest key taken; eq: how many of the keys equal to it are taken
+  unsigned long long cut = 0, prefix = 0;
+  int eq = 0, left = need, shift = 64;
+  while (left > 0) {
+    const int width = min(BITS, shift), next = shift - width;
+    for (int i = threadIdx.x; i < BINS; i += ST) bins[i] = 0;
+    if (threadIdx.x == 0) n_near = 0;
+    __syncthreads();
+    for (int c0 = 0; c0 < n; c0 += ST) {
+      const int c = c0 + threadIdx.x;
+      const bool in = c < n && (shift == 64 || keys[c] >> shift == prefix);
+      // neighbours in score share their top bits, so that lanes are counted together
+      const int digit = in ? (int)((keys[c] >> next) & ((1 << width) - 1)) : -1;
+      const unsigned same = __match_any_sync(0xffffffffu, digit);
+      if (in && lane == __ffs(same) - 1) atomicAdd(&bins[digit], __popc(same));
     }
     __syncthreads();
-    if (threadIdx.x == 0) {
-      int w = 0;
-      for (int i = 1; i < 8; ++i)
-        if (best_key[i] > best_key[w] || (best_key[i] == best_key[w] && best_page[i] < best_page[w])) w = i;
-      keys[best_page[w]] = KEY_TAKEN;
+    // the bin that holds the `left`-th highest: bins are scanned from the top
+    constexpr int PER = BINS / ST;
+    uint2 mine = make_uint2(0, 0), all;
+#pragma unroll
+    for (int i = 0; i < PER; ++i) mine.x += bins[BINS - 1 - (threadIdx.x * PER + i)];
+    int above = (int)scan_pair(mine, warp_sums, &all).x;
+#pragma unroll
+    for (int i = 0; i < PER; ++i) {
+      const int bin = BINS - 1 - (threadIdx.x * PER + i), count = bins[bin];
+      if (above < left && left <= above + count) {
+        bin_s = bin;
+        above_s = above;
+      }
+      above += count;
+    }
+    __syncthreads();
+    const int count = bins[bin_s];
+    prefix = shift == 64 ? (unsigned long long)bin_s : (prefix << width) | (unsigned long long)bin_s;
+    shift = next;
+    left -= above_s;
+    if (left == count || shift == 0) {
+      cut = prefix << shift;
+      eq = left;  // shift 0: `left` of the keys equal to the cut; otherwise every key of the bin
+      if (shift > 0) {  // one below the bin (no key is 0)
+        cut = cut ? cut - 1 : 0;
+        eq = 0;
+      }
+      break;
+    }
+    if (count <= ST) {  // few enough to compare all pairs
+      for (int c = threadIdx.x; c < n; c += ST)
+        if (keys[c] >> shift == prefix) near_key[atomicAdd(&n_near, 1)] = keys[c];
+      __syncthreads();
+      if ((int)threadIdx.x < count) {
+        const unsigned long long k = near_key[threadIdx.x];
+        int over = 0, same = 0;
+        for (int i = 0; i < count; ++i) {
+          over += near_key[i] > k;
+          same += near_key[i] == k;
+        }
+        if (over < left && left <= over + same) {  // equal keys write equal values
+          cut_s = k;
+          near_eq = left - over;
+        }
+      }
+      __syncthreads();
+      cut = cut_s;
+      eq = near_eq;
+      break;
     }
     __syncthreads();
   }
-  int done = 0;
-  for (int e0 = 0; e0 < held; e0 += 256) {
-    const int e = e0 + threadIdx.x;
-    const bool mine = e < held && keys[e] == KEY_TAKEN;
-    const unsigned m = __ballot_sync(0xffffffffu, mine);
-    if (lane == 0) counts[warp] = __popc(m);
-    __syncthreads();
-    int before = done;
-    for (int i = 0; i < 8; ++i) {
-      if (i < warp) before += counts[i];
-      done += counts[i];
-    }
-    if (mine) sel[before + __popc(m & ((1u << lane) - 1))] = e;
-    __syncthreads();
+  if (need == 0) {
+    cut = ~0ull;
+    eq = 0;
   }
+  // the chosen pages in order: every thread takes a run of pages
+  const int per = (n + ST - 1) / ST, c0 = min(n, (int)threadIdx.x * per), c1 = min(n, c0 + per);
+  uint2 mine = make_uint2(0, 0), all;
+  for (int c = c0; c < c1; ++c) {
+    mine.x += keys[c] > cut;
+    mine.y += keys[c] == cut;
+  }
+  const uint2 before = scan_pair(mine, warp_sums, &all);
+  int equal = (int)before.y, at = lo + (int)before.x + min(equal, eq);
+  for (int c = c0; c < c1; ++c) {
+    const bool take = keys[c] > cut || (keys[c] == cut && equal < eq);
+    equal += keys[c] == cut;
+    if (take) sel[at++] = lo + c;
+  }
+  for (int i = threadIdx.x; i < lo; i += ST) sel[i] = i;
+  for (int i = threadIdx.x; i < p.keep_last; i += ST) sel[p.budget - p.keep_last + i] = held - p.keep_last + i;
 }
 
 // ---------------------------------------------------------------------------------------
 // launchers
-
-cudaError_t pages_init_attributes() {
-  return cudaFuncSetAttribute(k_pages_plan, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)plan_smem(4096));
-}
 
 cudaError_t launch_pages_plan(const PlanParams &p, cudaStream_t st) {
   k_pages_plan<<<1, PT, plan_smem(p.batch), st>>>(p);
@@ -397,11 +521,42 @@ cudaError_t launch_pages_write(const WriteParams &p, int dtype, int src_dtype, c
   return cudaGetLastError();
 }
 
-cudaError_t launch_pages_select(const SelectParams &p, int dtype, cudaStream_t st) {
-  const dim3 grid(p.g.n_kv_heads, p.batch);
-  if (dtype == RTVLA_DTYPE_BF16) k_pages_select<bf16><<<grid, 256, 0, st>>>(p);
-  else k_pages_select<__half><<<grid, 256, 0, st>>>(p);
+namespace {
+size_t select_smem(const PageGeom &g) { return g.width <= SELECT_SMEM_KEYS ? (size_t)g.width * 8 : 0; }
+
+template <typename T, int D>
+cudaError_t select_attributes() {
+  return cudaFuncSetAttribute(k_pages_select<T, D>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                              SELECT_SMEM_KEYS * 8);
+}
+
+template <typename T>
+cudaError_t select(const SelectParams &p, cudaStream_t st) {
+  const dim3 grid(SC, p.g.n_kv_heads, p.batch);
+  const size_t sm = select_smem(p.g);
+  if (p.g.head_dim == 64) k_pages_select<T, 64><<<grid, ST, sm, st>>>(p);
+  else if (p.g.head_dim == 128) k_pages_select<T, 128><<<grid, ST, sm, st>>>(p);
+  else k_pages_select<T, 256><<<grid, ST, sm, st>>>(p);
   return cudaGetLastError();
+}
+}  // namespace
+
+cudaError_t pages_init_attributes() {
+  cudaError_t e =
+      cudaFuncSetAttribute(k_pages_plan, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)plan_smem(4096));
+  if (e == cudaSuccess) e = select_attributes<bf16, 64>();
+  if (e == cudaSuccess) e = select_attributes<bf16, 128>();
+  if (e == cudaSuccess) e = select_attributes<bf16, 256>();
+  if (e == cudaSuccess) e = select_attributes<__half, 64>();
+  if (e == cudaSuccess) e = select_attributes<__half, 128>();
+  if (e == cudaSuccess) e = select_attributes<__half, 256>();
+  return e;
+}
+
+bool pages_select_needs_keys(const PageGeom &g) { return g.width > SELECT_SMEM_KEYS; }
+
+cudaError_t launch_pages_select(const SelectParams &p, int dtype, cudaStream_t st) {
+  return dtype == RTVLA_DTYPE_BF16 ? select<bf16>(p, st) : select<__half>(p, st);
 }
 
 }  // namespace rtvla

@@ -25,7 +25,7 @@ struct rtvla_pages_ctx {
   float2 *rope_lo = nullptr, *rope_hi = nullptr;
   float *part_o = nullptr;
   float2 *part_ml = nullptr;
-  unsigned long long *keys = nullptr;  // select: [max_batch][n_kv_heads][table_width]
+  unsigned long long *keys = nullptr;  // select over long tables: [max_batch][n_kv_heads][table_width]
 };
 
 namespace {
@@ -126,7 +126,7 @@ rtvla_status p_create(rtvla_pages_ctx *c) {
   c->part_o = p_alloc<float>(c, parts * g.head_dim);
   c->part_ml = p_alloc<float2>(c, parts);
   if (!c->part_o || !c->part_ml) return RTVLA_ERR_OOM;
-  if (g.has_select) {
+  if (g.has_select && pages_select_needs_keys(c->g)) {
     c->keys = p_alloc<unsigned long long>(c, (size_t)g.max_batch * g.n_kv_heads * g.table_width);
     if (!c->keys) return RTVLA_ERR_OOM;
   }
@@ -258,7 +258,7 @@ rtvla_status rtvla_pages_select(rtvla_pages_ctx *c, int layer, const void *q, co
       (long long)keep_first + keep_last > budget)
     return RTVLA_ERR_INVALID_ARG;
   if (budget > 65536) return RTVLA_ERR_SHAPE;
-  if (!c->keys) return RTVLA_ERR_UNSUPPORTED;
+  if (!c->cfg.has_select) return RTVLA_ERR_UNSUPPORTED;
   OnDevice dev(c->device);
   if (!dev.ok) return RTVLA_ERR_CUDA;
   SelectParams p{c->g,     layer,    c->cfg.n_q_heads, kv->batch, q,       kv->k_mean, kv->table,

@@ -70,28 +70,40 @@ __device__ __forceinline__ int owner(const int *cum, int n, int i) {
 // popped page may be one pushed in the same step, so a pop looks its page up where the push would
 // read it instead of in the free list (pages pushed in this step lie at or above the old top, so
 // the pushes never touch an entry a pop reads).
+//
+// A decode step is one CTA: a chain of two scans and three dependent loads.  With more rows every
+// CTA repeats the scans and takes a share of the rows and pages; the last one to finish writes the
+// lengths and the new top, which the others still read (they may be updated in place).
 __global__ void __launch_bounds__(PT) k_pages_plan(PlanParams p) {
   extern __shared__ int sm[];
   __shared__ long long warp_sums[PT / 32];
-  __shared__ int first_refused;
+  __shared__ int first_refused, is_last;
   const PageGeom g = p.g;
   const int B = p.batch, cap = g.width << g.shift;
   int *s_len = sm;                  // length before the step; ~length: refused alone
-  int *s_rows = s_len + B;          // [B + 1] rows before request b, at most n_rows
+  int *s_delta = s_len + B;
+  int *s_rows = s_delta + B;        // [B + 1] rows before request b, at most n_rows
   int *s_take = s_rows + B + 1;     // [B + 1] pages popped before request b
   int *s_back = s_take + B + 1;     // [B + 1] pages pushed before request b
   const int per = (B + PT - 1) / PT;
   const int b0 = min(B, (int)threadIdx.x * per), b1 = min(B, b0 + per);
+  const int first = blockIdx.x * PT + threadIdx.x, stride = gridDim.x * PT;  // shares of rows and pages
   bool bad = false;
   if (threadIdx.x == 0) first_refused = B;
+  for (int b = threadIdx.x; b < B; b += PT) {
+    s_len[b] = p.lens[b];
+    s_delta[b] = p.delta[b];
+  }
+  const int raw_free = p.n_free[0];
+  __syncthreads();
 
   long long sum = 0, total;
-  for (int b = b0; b < b1; ++b) sum += max(p.delta[b], 0);
+  for (int b = b0; b < b1; ++b) sum += max(s_delta[b], 0);
   long long rows = block_scan(sum, &total, warp_sums);
   if (threadIdx.x == 0) s_rows[B] = (int)min(total, (long long)p.n_rows);
   long long take = 0, back = 0;
   for (int b = b0; b < b1; ++b) {
-    const int raw = p.lens[b], delta = p.delta[b];
+    const int raw = s_len[b], delta = s_delta[b];
     bool alone = false;
     const int len = pg_len(raw, g, &alone);
     s_rows[b] = (int)min(rows, (long long)p.n_rows);
@@ -110,7 +122,6 @@ __global__ void __launch_bounds__(PT) k_pages_plan(PlanParams p) {
   long long all_take, all_back;
   take = block_scan(take, &all_take, warp_sums);
   back = block_scan(back, &all_back, warp_sums);
-  const int raw_free = p.n_free[0];
   const int nf = min(max(raw_free, 0), g.n_pages);
   // a table that gives back more pages than the pool has is the caller's fault
   const int n_back = (int)min(all_back, (long long)(g.n_pages - nf));
@@ -121,7 +132,7 @@ __global__ void __launch_bounds__(PT) k_pages_plan(PlanParams p) {
     s_back[b] = (int)min(back, (long long)n_back);
     const int len = s_len[b];
     if (len >= 0) {
-      const int held = pg_pages(len, g), after = pg_pages((int)max(0ll, (long long)len + p.delta[b]), g);
+      const int held = pg_pages(len, g), after = pg_pages((int)max(0ll, (long long)len + s_delta[b]), g);
       if (after > held && take + (after - held) > top) atomicMin(&first_refused, b);
       take += max(0, after - held);
       back += max(0, held - after);
@@ -145,12 +156,12 @@ __global__ void __launch_bounds__(PT) k_pages_plan(PlanParams p) {
     const int at = top - 1 - i;
     return at < nf ? p.free_pages[at] : given_back(at - nf);
   };
-  for (int i = threadIdx.x; i < n_take; i += PT) {
+  for (int i = first; i < n_take; i += stride) {
     const int b = owner(s_take, B, i);
     p.table[(size_t)b * g.width + pg_pages(s_len[b], g) + (i - s_take[b])] = popped(i);
   }
-  for (int e = threadIdx.x; e < n_back; e += PT) p.free_pages[nf + e] = given_back(e);
-  for (int r = threadIdx.x; r < p.n_rows; r += PT) {
+  for (int e = first; e < n_back; e += stride) p.free_pages[nf + e] = given_back(e);
+  for (int r = first; r < p.n_rows; r += stride) {
     int slot = -1, pos = 0;
     if (r < s_rows[B]) {
       const int b = owner(s_rows, B, r), len = s_len[b];
@@ -169,11 +180,21 @@ __global__ void __launch_bounds__(PT) k_pages_plan(PlanParams p) {
     p.slots[r] = slot;
     p.positions[r] = pos;
   }
-  __syncthreads();  // lens_out may be lens, n_free_out n_free
+  if (bad) set_error(p.ctl, DEVERR_BOUNDS, PG_AT_PLAN);
+  if (gridDim.x > 1) {
+    __syncthreads();  // this CTA has read its lengths
+    if (threadIdx.x == 0) {
+      __threadfence();
+      is_last = atomicAdd(p.done, 1) == (int)gridDim.x - 1;
+    }
+    __syncthreads();
+    if (!is_last) return;
+    if (threadIdx.x == 0) *p.done = 0;  // for the next call
+  }
   for (int b = threadIdx.x; b < B; b += PT) {
     const int len = s_len[b];
     int n = len < 0 ? ~len : len;
-    if (len >= 0 && (b < stop || s_take[b + 1] == s_take[b])) n = (int)max(0ll, (long long)len + p.delta[b]);
+    if (len >= 0 && (b < stop || s_take[b + 1] == s_take[b])) n = (int)max(0ll, (long long)len + s_delta[b]);
     p.lens_out[b] = n;
     p.row_start[b] = s_rows[b];
   }
@@ -181,11 +202,10 @@ __global__ void __launch_bounds__(PT) k_pages_plan(PlanParams p) {
     p.row_start[B] = s_rows[B];
     p.n_free_out[0] = top - n_take;
   }
-  if (bad) set_error(p.ctl, DEVERR_BOUNDS, PG_AT_PLAN);
 }
 
 namespace {
-size_t plan_smem(int batch) { return (size_t)(4 * batch + 3) * sizeof(int); }
+size_t plan_smem(int batch) { return (size_t)(5 * batch + 3) * sizeof(int); }
 
 // ---------------------------------------------------------------------------------------
 // write
@@ -504,8 +524,10 @@ __global__ void __cluster_dims__(SC, 1, 1) __launch_bounds__(ST) k_pages_select(
 // ---------------------------------------------------------------------------------------
 // launchers
 
-cudaError_t launch_pages_plan(const PlanParams &p, cudaStream_t st) {
-  k_pages_plan<<<1, PT, plan_smem(p.batch), st>>>(p);
+cudaError_t launch_pages_plan(const PlanParams &p, int sm_count, cudaStream_t st) {
+  // four rows per thread: the scans cost every CTA about 4 us, as much as a thread's four rows
+  const int want = (p.n_rows + 4 * PT - 1) / (4 * PT);
+  k_pages_plan<<<want < 1 ? 1 : want < sm_count ? want : sm_count, PT, plan_smem(p.batch), st>>>(p);
   return cudaGetLastError();
 }
 

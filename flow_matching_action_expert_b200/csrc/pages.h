@@ -26,10 +26,11 @@ struct PlanParams {
   int32_t *row_start;
   int batch;
   int n_rows;
+  int *done;  // workspace: CTAs finished, 0 between calls
   DevCtl *ctl;
 };
 cudaError_t pages_init_attributes();
-cudaError_t launch_pages_plan(const PlanParams &p, cudaStream_t st);
+cudaError_t launch_pages_plan(const PlanParams &p, int sm_count, cudaStream_t st);
 
 struct WriteParams {
   PageGeom g;

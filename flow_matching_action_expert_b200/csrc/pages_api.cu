@@ -23,6 +23,7 @@ struct rtvla_pages_ctx {
   GuardRegion *d_guards = nullptr;
   DevCtl *ctl = nullptr;
   float2 *rope_lo = nullptr, *rope_hi = nullptr;
+  int *done = nullptr;  // plan: CTAs finished
   float *part_o = nullptr;
   float2 *part_ml = nullptr;
   unsigned long long *keys = nullptr;  // select over long tables: [max_batch][n_kv_heads][table_width]
@@ -112,7 +113,9 @@ rtvla_status p_create(rtvla_pages_ctx *c) {
     return RTVLA_ERR_CUDA;
   if (pages_init_attributes() != cudaSuccess || pages_attend_init_attributes() != cudaSuccess) return RTVLA_ERR_CUDA;
   c->ctl = p_alloc<DevCtl>(c, 1);
-  if (!c->ctl) return RTVLA_ERR_OOM;
+  c->done = p_alloc<int>(c, 1);
+  if (!c->ctl || !c->done) return RTVLA_ERR_OOM;
+  if (cudaMemset(c->done, 0, sizeof(int)) != cudaSuccess) return RTVLA_ERR_CUDA;
   if (g.rope_theta > 0.f) {
     const int hi = ((g.table_width * g.page_size - 1) >> 8) + 1;
     c->rope_lo = p_alloc<float2>(c, (size_t)256 * (g.head_dim / 2));
@@ -212,8 +215,8 @@ rtvla_status rtvla_pages_plan(rtvla_pages_ctx *c, const int32_t *lens, const int
   OnDevice dev(c->device);
   if (!dev.ok) return RTVLA_ERR_CUDA;
   PlanParams p{c->g,     lens,       delta, free_pages, n_free,    kv->table, kv->lens,
-               n_free_out, slots, positions, row_start, kv->batch, n_rows, c->ctl};
-  return launched(launch_pages_plan(p, static_cast<cudaStream_t>(stream)));
+               n_free_out, slots, positions, row_start, kv->batch, n_rows, c->done, c->ctl};
+  return launched(launch_pages_plan(p, c->sm_count, static_cast<cudaStream_t>(stream)));
 }
 
 rtvla_status rtvla_pages_write(rtvla_pages_ctx *c, int layer, const void *qkv, int qkv_dtype, const int32_t *slots,

@@ -295,83 +295,116 @@ namespace {
 constexpr int ST = 512;            // threads of a select CTA
 constexpr int SC = 8;              // CTAs of a cluster: they score, the first one chooses
 constexpr int RUN = 16;            // pages a warp scores at a time
-constexpr int BITS = 11, BINS = 1 << BITS;
-constexpr int SELECT_SMEM_KEYS = 8192;  // keys held in shared memory; longer tables use the workspace
+constexpr int BITS = 9, BINS = 1 << BITS;  // one bin per thread
+constexpr int NEAR = 64;           // pages scored again and compared in all pairs
+constexpr int SELECT_SMEM_KEYS = 16384;  // candidates whose keys fit shared memory
 
-// Order-preserving map of a score to an integer; 0 and 1 are kept for pages outside the pool.
-__device__ __forceinline__ unsigned long long score_key(double s) {
+// Order-preserving maps of scores to integers; 0 (fp32) and 1 (fp64) are kept for pages outside
+// the pool, 0 (fp64) for pages that are out already.
+__device__ __forceinline__ uint32_t key32(float s) {
+  const uint32_t u = __float_as_uint(s);
+  return max((u >> 31) ? ~u : u | 0x80000000u, 1u);
+}
+__device__ __forceinline__ float score32(uint32_t k) {
+  return __uint_as_float(k >> 31 ? k & 0x7fffffffu : ~k);
+}
+__device__ __forceinline__ unsigned long long key64(double s) {
   const unsigned long long u = (unsigned long long)__double_as_longlong(s);
-  return max((u >> 63) ? ~u : u | 0x8000000000000000ull, 2ull);
+  return min(max((u >> 63) ? ~u : u | 0x8000000000000000ull, 2ull), ~1ull);
 }
-constexpr unsigned long long KEY_BAD = 1;
 
-__device__ __forceinline__ void add8(double (&a)[8], const uint4 &v, bf16) {
+// the eight 16-bit values of v in fp32 (exact)
+__device__ __forceinline__ void unpack8(float (&f)[8], const uint4 &v, bf16) {
   const uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    a[2 * i] += (double)__uint_as_float(w[i] << 16);
-    a[2 * i + 1] += (double)__uint_as_float(w[i] & 0xffff0000u);
+    f[2 * i] = __uint_as_float(w[i] << 16);
+    f[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
   }
 }
-__device__ __forceinline__ void add8(double (&a)[8], const uint4 &v, __half) {
+__device__ __forceinline__ void unpack8(float (&f)[8], const uint4 &v, __half) {
   const uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&w[i]));
-    a[2 * i] += (double)f.x;
-    a[2 * i + 1] += (double)f.y;
+    const float2 x = __half22float2(*reinterpret_cast<const __half2 *>(&w[i]));
+    f[2 * i] = x.x;
+    f[2 * i + 1] = x.y;
   }
 }
 
-// Exclusive scan of a pair of counts over the block.
-__device__ uint2 scan_pair(uint2 v, uint2 *warp_sums, uint2 *total) {
+// Exclusive scan of one count per thread over the block; total receives the sum.
+__device__ int scan_count(int v, int *warp_sums, int &total) {
   const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
-  uint2 inc = v;
+  auto inclusive = [lane](int x) {
 #pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const unsigned x = __shfl_up_sync(0xffffffffu, inc.x, o), y = __shfl_up_sync(0xffffffffu, inc.y, o);
-    if (lane >= o) {
-      inc.x += x;
-      inc.y += y;
+    for (int o = 1; o < 32; o <<= 1) {
+      const int a = __shfl_up_sync(0xffffffffu, x, o);
+      if (lane >= o) x += a;
     }
-  }
+    return x;
+  };
+  const int inc = inclusive(v);
   __syncthreads();
   if (lane == 31) warp_sums[w] = inc;
   __syncthreads();
-  uint2 before = make_uint2(0, 0), all = make_uint2(0, 0);
-#pragma unroll
-  for (int i = 0; i < ST / 32; ++i) {
-    const uint2 x = warp_sums[i];
-    if (i < w) {
-      before.x += x.x;
-      before.y += x.y;
-    }
-    all.x += x.x;
-    all.y += x.y;
-  }
-  *total = all;
-  return make_uint2(before.x + inc.x - v.x, before.y + inc.y - v.y);
+  const int sums = inclusive(lane < ST / 32 ? warp_sums[lane] : 0);
+  const int before = __shfl_sync(0xffffffffu, sums, (w + 31) & 31);
+  total = __shfl_sync(0xffffffffu, sums, 31);
+  return (w ? before : 0) + inc - v;
 }
 
 }  // namespace
 
-// One cluster per request and KV head.  Its CTAs share the scoring (16 bytes of a page's mean per
-// lane, fp64 sums: the means of a long request are a few hundred KB, so this is latency, not
-// bandwidth) and put order-preserving integer keys into the first CTA's shared memory.  That CTA
-// finds the lowest key taken by radix passes from the top bits, which stop as soon as the pages
-// in the deciding bin fit one comparison of all pairs: two passes for ordinary scores.  Selected is
-// then every key above that one, and of the keys equal to it the first few in page order.
+// One cluster per request and KV head.  The choice is defined by fp64 scores, but this GPU adds
+// fp64 numbers some ten times slower than fp32 ones (scoring 2040 pages of 256 components took
+// 12000 of 22000 cycles), so the cluster scores in fp32, 16 bytes of a page's mean per lane, and
+// puts order-preserving integer keys into the first CTA's shared memory.  An fp32 score is within
+//   E = 16 * 2^-24 * sum_i |q_i| * max |mean|
+// of the exact one (8 products and sums in a lane, at most 5 sums over lanes, one rounding of q:
+// 14 roundings).  With t the `need`-th highest fp32 score, the `need`-th highest exact one lies
+// within E of t: pages above t + 2E are in, pages below t - 2E are out, and only those between are
+// scored again in fp64 - with ordinary scores the page at t alone.
+//
+// t is found by one histogram over equal steps of the score and a comparison of all pairs in the
+// deciding step; where that step holds too many (or a bound is not finite), radix passes over the
+// keys' bits find it for any values.  If more than NEAR pages lie within 2E of t (equal means,
+// scores near zero, NaN), the same radix passes run over fp64 keys in a workspace.
 template <typename T, int D>
-__global__ void __cluster_dims__(SC, 1, 1) __launch_bounds__(ST) k_pages_select(SelectParams p) {
-  extern __shared__ unsigned long long smem_keys[];
-  __shared__ int bins[BINS];
-  __shared__ uint2 warp_sums[ST / 32];
-  __shared__ unsigned long long near_key[ST];
-  __shared__ int bin_s, above_s, n_near, near_eq;
-  __shared__ unsigned long long cut_s;
+__global__ void __cluster_dims__(SC, 1, 1) __launch_bounds__(ST, 2) k_pages_select(SelectParams p) {
+  extern __shared__ uint32_t smem_keys[];
+  __shared__ double q_sum[D];
+  __shared__ float q_32[D];
+  __shared__ int bins[BINS], warp_sums[ST / 32];
+  __shared__ uint32_t ends[2][ST / 32], big_mean[SC * (ST / 32)], near_key[NEAR];
+  __shared__ unsigned long long near_key64[NEAR];
+  __shared__ int near_c[NEAR];
+  __shared__ float q_size[ST / 32];
+  __shared__ int found[3], n_near, n_over;
+  __shared__ uint32_t cut_s;
   const PageGeom g = p.g;
   const int rank = blockIdx.x, h = blockIdx.y, b = blockIdx.z, G = p.n_q_heads / g.n_kv_heads;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  constexpr int LPP = D / 8, PPW = 32 / LPP;  // lanes per page, pages per load
+  const int sub = lane / LPP, ln = lane % LPP;
+  // the sum of the group's query heads, one component per thread; loads that need no length first
+  const int32_t *row = p.table + (size_t)b * g.width;
+  const int lo = p.keep_first, my_c0 = (warp * SC + rank) * RUN;
+  const int raw_page = lane < RUN && lo + my_c0 + lane < g.width ? row[lo + my_c0 + lane] : -1;
+  if (threadIdx.x < D) {
+    const T *q = static_cast<const T *>(p.q) + ((size_t)b * p.n_q_heads + h * G) * D + threadIdx.x;
+    double sum = 0.0;
+    for (int j0 = 0; j0 < G; j0 += 8) {
+      T v[8];
+#pragma unroll
+      for (int j = 0; j < 8; ++j) v[j] = j0 + j < G ? q[(size_t)(j0 + j) * D] : from_f<T>(0.f);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) sum += (double)to_f(v[j]);
+    }
+    q_sum[threadIdx.x] = sum;
+    q_32[threadIdx.x] = (float)sum;
+    const float size = warp_sum(fabsf((float)sum));
+    if (lane == 0) q_size[warp] = size;
+  }
   bool bad = false;
   const int held = pg_pages(pg_len(p.lens[b], g, &bad), g);
   if (bad && threadIdx.x == 0 && rank == 0 && h == 0) set_error(p.ctl, DEVERR_BOUNDS, PG_AT_SELECT);
@@ -381,141 +414,304 @@ __global__ void __cluster_dims__(SC, 1, 1) __launch_bounds__(ST) k_pages_select(
     return;
   }
   // candidates: logical pages lo .. lo + n - 1, of which `need` are chosen
-  const int lo = p.keep_first, n = held - p.keep_last - lo, need = p.budget - lo - p.keep_last;
+  const int n = held - p.keep_last - lo, need = p.budget - lo - p.keep_last;
+  // fp32 keys: in shared memory, or for long tables in the lower halves of the workspace's words
   const bool in_smem = g.width <= SELECT_SMEM_KEYS;
-  unsigned long long *keys = in_smem ? smem_keys : p.keys + ((size_t)b * g.n_kv_heads + h) * g.width;
+  unsigned long long *wide = p.keys + ((size_t)b * g.n_kv_heads + h) * g.width;
+  uint32_t *keys = in_smem ? smem_keys : reinterpret_cast<uint32_t *>(wide);
+  const int ks = in_smem ? 1 : 2;
   {
-    unsigned long long *dst = keys;
-    if (in_smem) {
+    auto in_first = [](void *x) {  // the same variable of the cluster's first CTA
       uint64_t at;
-      asm("mapa.u64 %0, %1, %2;" : "=l"(at) : "l"(reinterpret_cast<uint64_t>(smem_keys)), "r"(0));
-      dst = reinterpret_cast<unsigned long long *>(at);
-    }
-    constexpr int LPP = D / 8, PPW = 32 / LPP;  // lanes per page, pages per load
-    const int sub = lane / LPP, ln = lane % LPP;
-    double qs[8] = {0, 0, 0, 0, 0, 0, 0, 0};
-    const T *q = static_cast<const T *>(p.q) + ((size_t)b * p.n_q_heads + h * G) * D + ln * 8;
-    for (int j = 0; j < G; ++j) add8(qs, *reinterpret_cast<const uint4 *>(q + (size_t)j * D), T());
-    for (int c0 = (rank * (ST / 32) + warp) * RUN; c0 < n; c0 += SC * (ST / 32) * RUN) {
-      const int mine = lane < RUN && c0 + lane < n ? pg_page(p.table + (size_t)b * g.width, lo + c0 + lane, g) : -1;
-      if (lane < RUN && c0 + lane < n && mine < 0) bad = true;
-      constexpr int LOADS = RUN / PPW, AHEAD = LOADS < 8 ? LOADS : 8;
+      asm("mapa.u64 %0, %1, %2;" : "=l"(at) : "l"(reinterpret_cast<uint64_t>(x)), "r"(0));
+      return reinterpret_cast<void *>(at);
+    };
+    uint32_t *dst = in_smem ? static_cast<uint32_t *>(in_first(smem_keys)) : keys;
+    __syncthreads();  // q_32
+    float q[8], big = 0.f;
 #pragma unroll
-      for (int i0 = 0; i0 < LOADS; i0 += AHEAD) {
-        uint4 v[AHEAD];
-        int page[AHEAD];
+    for (int u = 0; u < 8; ++u) q[u] = q_32[ln * 8 + u];
+    for (int c0 = my_c0; c0 < n; c0 += SC * (ST / 32) * RUN) {
+      int mine = c0 == my_c0 ? raw_page : lane < RUN && c0 + lane < n ? row[lo + c0 + lane] : -1;
+      if (lane >= RUN || c0 + lane >= n) mine = -1;
+      else if (mine < 0 || mine >= g.n_pages) {
+        bad = true;
+        mine = -1;
+      }
+      // the page's number among all layers' and heads' means; page 0 in place of a missing one
+      const uint32_t mean_at = ((uint32_t)p.layer * g.n_pages + (uint32_t)max(mine, 0)) * g.n_kv_heads + h;
+      constexpr int LOADS = LPP / 2 < 8 ? LPP / 2 : 8, STEP = LOADS * PPW;  // loads in flight, their pages
+      static_assert(RUN % STEP == 0, "whole steps");
 #pragma unroll
-        for (int i = 0; i < AHEAD; ++i) {
-          page[i] = __shfl_sync(0xffffffffu, mine, (i0 + i) * PPW + sub);
-          v[i] = make_uint4(0, 0, 0, 0);
-          if (page[i] >= 0)
-            v[i] = *reinterpret_cast<const uint4 *>(static_cast<const T *>(p.k_mean) +
-                                                    pg_mean_elem(p.layer, page[i], h, g) + ln * 8);
+      for (int i0 = 0; i0 < RUN; i0 += STEP) {
+        uint4 v[LOADS];
+#pragma unroll
+        for (int i = 0; i < LOADS; ++i) {
+          const uint32_t m = __shfl_sync(0xffffffffu, mean_at, i0 + i * PPW + sub);
+          v[i] = *reinterpret_cast<const uint4 *>(static_cast<const T *>(p.k_mean) + (size_t)m * D + ln * 8);
         }
+        float s[LOADS];  // this lane's share of the scores of pages i0 + i * PPW + sub
 #pragma unroll
-        for (int i = 0; i < AHEAD; ++i) {
-          double m[8] = {0, 0, 0, 0, 0, 0, 0, 0}, s = 0.0;
-          add8(m, v[i], T());
+        for (int i = 0; i < LOADS; ++i) {
+          float f[8];
+          unpack8(f, v[i], T());
+          s[i] = 0.f;
 #pragma unroll
-          for (int u = 0; u < 8; ++u) s += qs[u] * m[u];
-#pragma unroll
-          for (int o = LPP / 2; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
-          const int c = c0 + (i0 + i) * PPW + sub;
-          if (ln == 0 && c < n) dst[c] = page[i] < 0 ? KEY_BAD : score_key(s);
+          for (int u = 0; u < 8; u += 2) {
+            s[i] = fmaf(q[u], f[u], s[i]);
+            s[i] = fmaf(q[u + 1], f[u + 1], s[i]);
+            big = fmaxf(big, fmaxf(fabsf(f[u]), fabsf(f[u + 1])));
+          }
+          if (!(fabsf(s[i]) < INFINITY)) big = INFINITY;  // no bound: all pages go by fp64
         }
+        // sums over the LPP lanes of a page; the first steps halve the pages a lane holds
+        int i = 0;
+#pragma unroll
+        for (int o = LPP / 2, w = LOADS / 2; o > 0; o >>= 1, w >>= 1) {
+          if (w > 0) {
+            const bool up = lane & o;
+            if (up) i += w;
+#pragma unroll
+            for (int u = 0; u < w; ++u) {
+              const float give = up ? s[u] : s[u + w], keep = up ? s[u + w] : s[u];
+              s[u] = keep + __shfl_xor_sync(0xffffffffu, give, o);
+            }
+          } else {
+            s[0] += __shfl_xor_sync(0xffffffffu, s[0], o);
+          }
+        }
+        const int at = i0 + i * PPW + sub, page = __shfl_sync(0xffffffffu, mine, at);
+        if (!(lane & (LPP / LOADS - 1)) && c0 + at < n) dst[(c0 + at) * ks] = page < 0 ? 0 : key32(s[0]);
       }
     }
+    const uint32_t most = __reduce_max_sync(0xffffffffu, __float_as_uint(big));  // not negative: ordered as bits
+    if (lane == 0) static_cast<uint32_t *>(in_first(big_mean))[rank * (ST / 32) + warp] = most;
     if (bad) set_error(p.ctl, DEVERR_BOUNDS, PG_AT_SELECT);
   }
   asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
   if (rank != 0) return;
 
-  // cut: the lowest key taken; eq: how many of the keys equal to it are taken
-  unsigned long long cut = 0, prefix = 0;
-  int eq = 0, left = need, shift = 64;
-  while (left > 0) {
-    const int width = min(BITS, shift), next = shift - width;
-    for (int i = threadIdx.x; i < BINS; i += ST) bins[i] = 0;
-    if (threadIdx.x == 0) n_near = 0;
+  // histogram of digit_of(c) (-1: none); the bin that holds the `left`-th highest, the number in
+  // the bins above it and in it
+  int above, count;
+  auto find = [&](int left, bool together, auto digit_of) {
+    bins[threadIdx.x] = 0;
+    if (threadIdx.x == 0) n_near = n_over = 0;
     __syncthreads();
     for (int c0 = 0; c0 < n; c0 += ST) {
-      const int c = c0 + threadIdx.x;
-      const bool in = c < n && (shift == 64 || keys[c] >> shift == prefix);
-      // neighbours in score share their top bits, so that lanes are counted together
-      const int digit = in ? (int)((keys[c] >> next) & ((1 << width) - 1)) : -1;
-      const unsigned same = __match_any_sync(0xffffffffu, digit);
-      if (in && lane == __ffs(same) - 1) atomicAdd(&bins[digit], __popc(same));
+      const int c = c0 + threadIdx.x, digit = c < n ? digit_of(c) : -1;
+      if (together) {  // top bits are shared by many keys: equal lanes are counted at once
+        const unsigned same = __match_any_sync(0xffffffffu, digit);
+        if (digit >= 0 && lane == __ffs(same) - 1) atomicAdd(&bins[digit], __popc(same));
+      } else if (digit >= 0) {
+        atomicAdd(&bins[digit], 1);
+      }
     }
     __syncthreads();
-    // the bin that holds the `left`-th highest: bins are scanned from the top
-    constexpr int PER = BINS / ST;
-    uint2 mine = make_uint2(0, 0), all;
-#pragma unroll
-    for (int i = 0; i < PER; ++i) mine.x += bins[BINS - 1 - (threadIdx.x * PER + i)];
-    int above = (int)scan_pair(mine, warp_sums, &all).x;
-#pragma unroll
-    for (int i = 0; i < PER; ++i) {
-      const int bin = BINS - 1 - (threadIdx.x * PER + i), count = bins[bin];
-      if (above < left && left <= above + count) {
-        bin_s = bin;
-        above_s = above;
-      }
-      above += count;
+    static_assert(BINS == ST, "one bin per thread");
+    int total;
+    const int bin = BINS - 1 - threadIdx.x, have = bins[bin], over = scan_count(have, warp_sums, total);
+    if (over < left && left <= over + have) {
+      found[0] = bin;
+      found[1] = over;
+      found[2] = have;
     }
     __syncthreads();
-    const int count = bins[bin_s];
-    prefix = shift == 64 ? (unsigned long long)bin_s : (prefix << width) | (unsigned long long)bin_s;
-    shift = next;
-    left -= above_s;
-    if (left == count || shift == 0) {
-      cut = prefix << shift;
-      eq = left;  // shift 0: `left` of the keys equal to the cut; otherwise every key of the bin
-      if (shift > 0) {  // one below the bin (no key is 0)
-        cut = cut ? cut - 1 : 0;
-        eq = 0;
-      }
-      break;
+    above = found[1];
+    count = found[2];
+    return found[0];
+  };
+
+  // chosen are the candidates with keys from `cut` on
+  uint32_t cut = ~0u;
+  if (need > 0) {
+    uint32_t kmin = ~0u, kmax = 0;
+    for (int c = threadIdx.x; c < n; c += ST) {
+      const uint32_t k = keys[c * ks];
+      kmin = min(kmin, k);
+      kmax = max(kmax, k);
     }
-    if (count <= ST) {  // few enough to compare all pairs
+    kmin = __reduce_min_sync(0xffffffffu, kmin);
+    kmax = __reduce_max_sync(0xffffffffu, kmax);
+    if (lane == 0) {
+      ends[0][warp] = kmin;
+      ends[1][warp] = kmax;
+    }
+    __syncthreads();
+    kmin = __reduce_min_sync(0xffffffffu, ends[0][lane % (ST / 32)]);
+    kmax = __reduce_max_sync(0xffffffffu, ends[1][lane % (ST / 32)]);
+    uint32_t most = 0;
+#pragma unroll
+    for (int i = 0; i < SC * (ST / 32) / 32; ++i) most = max(most, big_mean[i * 32 + lane]);
+    most = __reduce_max_sync(0xffffffffu, most);
+    const float size = warp_sum(lane < D / 32 ? q_size[lane] : 0.f);
+    // (the last term: products below the smallest normal fp32 number)
+    const float E = 16.f * 5.9604645e-8f * size * __uint_as_float(most) + 1e-42f;
+
+    // t, the `need`-th highest fp32 key
+    uint32_t t = 0;
+    auto settle = [&](int left, auto is_near) {  // the `left`-th highest of the `count` <= NEAR keys picked
       for (int c = threadIdx.x; c < n; c += ST)
-        if (keys[c] >> shift == prefix) near_key[atomicAdd(&n_near, 1)] = keys[c];
+        if (is_near(c)) near_key[atomicAdd(&n_near, 1)] = keys[c * ks];
       __syncthreads();
       if ((int)threadIdx.x < count) {
-        const unsigned long long k = near_key[threadIdx.x];
+        const uint32_t k = near_key[threadIdx.x];
         int over = 0, same = 0;
         for (int i = 0; i < count; ++i) {
           over += near_key[i] > k;
           same += near_key[i] == k;
         }
-        if (over < left && left <= over + same) {  // equal keys write equal values
-          cut_s = k;
-          near_eq = left - over;
-        }
+        if (over < left && left <= over + same) cut_s = k;  // equal keys write equal values
       }
       __syncthreads();
-      cut = cut_s;
-      eq = near_eq;
-      break;
+      t = cut_s;
+    };
+    const float low = score32(kmin), scale = (BINS - 1) / (score32(kmax) - low);
+    bool done = false;
+    if (low - low == 0.f && scale > 0.f && scale - scale == 0.f) {  // all finite, and not all equal
+      // (s - low) * scale rises with s, rounded or not
+      auto step = [&](int c) { return min(BINS - 1, (int)((score32(keys[c * ks]) - low) * scale)); };
+      const int bin = find(need, false, step);
+      if (count <= NEAR) {
+        settle(need - above, [&](int c) { return step(c) == bin; });
+        done = true;
+      }
+    }
+    uint32_t prefix = 0;
+    for (int left = need, shift = 32; !done;) {
+      const int width = min(BITS, shift), next = shift - width;
+      const int bin = find(left, true, [&](int c) {
+        const uint32_t k = keys[c * ks];
+        return shift == 32 || k >> shift == prefix ? (int)(k >> next & ((1u << width) - 1)) : -1;
+      });
+      prefix = shift == 32 ? (uint32_t)bin : prefix << width | (uint32_t)bin;
+      shift = next;
+      left -= above;
+      done = shift == 0 || count <= NEAR;
+      if (shift == 0) t = prefix;
+      else if (count <= NEAR) settle(left, [&](int c) { return keys[c * ks] >> shift == prefix; });
+      __syncthreads();
+    }
+
+    // pages within 2E of t (all of them, if there is no bound)
+    const float ts = score32(t), reach = 2.f * E;
+    const bool bounded = t != 0 && ts - ts == 0.f && reach - reach == 0.f;
+    cut = bounded ? key32(__fadd_rd(ts, -reach)) : 0;
+    const uint32_t top = bounded ? key32(__fadd_ru(ts, reach)) : ~0u;
+    if (threadIdx.x == 0) n_near = n_over = 0;
+    __syncthreads();
+    for (int c0 = 0; c0 < n; c0 += ST) {
+      const int c = c0 + threadIdx.x;
+      const uint32_t k = c < n ? keys[c * ks] : 0;
+      const bool over = c < n && k > top, within = c < n && k >= cut && !over;
+      const unsigned all = __ballot_sync(0xffffffffu, over);
+      if (lane == 0 && all) atomicAdd(&n_over, __popc(all));
+      if (within) {
+        const int at = atomicAdd(&n_near, 1);
+        if (at < NEAR) near_c[at] = c;
+      }
     }
     __syncthreads();
+    const int zone = n_near, left = need - n_over;
+    // a whole warp: the exact score of candidate c
+    auto exact = [&](int c) {
+      const int page = pg_page(row, lo + c, g);
+      if (page < 0) return 1ull;
+      const T *m = static_cast<const T *>(p.k_mean) + pg_mean_elem(p.layer, page, h, g);
+      double s = 0.0;
+#pragma unroll
+      for (int i = 0; i < D / 32; ++i) s += q_sum[lane + 32 * i] * (double)to_f(m[lane + 32 * i]);
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+      return key64(s);
+    };
+    if (zone == left) {
+      // all of them
+    } else if (zone <= NEAR) {
+      for (int i = warp; i < zone; i += ST / 32) {
+        const unsigned long long k = exact(near_c[i]);
+        if (lane == 0) near_key64[i] = k;
+      }
+      __syncthreads();
+      if ((int)threadIdx.x < zone) {
+        const unsigned long long k = near_key64[threadIdx.x];
+        const int c = near_c[threadIdx.x];
+        int better = 0;
+        for (int i = 0; i < zone; ++i)
+          better += near_key64[i] > k || (near_key64[i] == k && near_c[i] < c);
+        if (better >= left) keys[c * ks] = 0;
+        else if (cut == 0) keys[c * ks] = 1;
+      }
+      cut = max(cut, 1u);
+      __syncthreads();
+    } else {
+      // fp64 keys of the pages between in the workspace (all ones for those in, 0 for those out),
+      // then the same passes: the cut, and of the pages equal to it the first ones
+      for (int c = warp; c < n; c += ST / 32) {
+        const uint32_t k = keys[c * ks];
+        const unsigned long long w = k > top ? ~0ull : k >= cut ? exact(c) : 0;
+        __syncwarp();
+        if (lane == 0) wide[c] = w;
+        __syncwarp();
+      }
+      __syncthreads();
+      unsigned long long pre = 0;
+      int eq = need, total = 0;
+      for (int shift = 64; shift > 0;) {
+        const int width = min(BITS, shift), next = shift - width;
+        const int bin = find(eq, true, [&](int c) {
+          const unsigned long long k = wide[c];
+          return k && (shift == 64 || k >> shift == pre) ? (int)(k >> next & ((1u << width) - 1)) : -1;
+        });
+        pre = shift == 64 ? (unsigned long long)bin : pre << width | (unsigned long long)bin;
+        shift = next;
+        eq -= above;
+        total = count;
+        __syncthreads();
+      }
+      int last = n - 1;  // the last index taken of those equal to the cut
+      if (total > eq) {
+        unsigned pre_i = 0;
+        int want = eq;
+        constexpr int IDX_BITS = 27;  // three passes over the complement of the index
+        for (int shift = IDX_BITS; shift > 0; shift -= BITS) {
+          const int next = shift - BITS;
+          const int bin = find(want, true, [&](int c) {
+            const unsigned i = (1u << IDX_BITS) - 1 - (unsigned)c;
+            return wide[c] == pre && (shift == IDX_BITS || i >> shift == pre_i) ? (int)(i >> next & (BINS - 1)) : -1;
+          });
+          pre_i = pre_i << BITS | (unsigned)bin;
+          want -= above;
+          __syncthreads();
+        }
+        last = (int)((1u << IDX_BITS) - 1 - pre_i);
+      }
+      // 1: chosen, 0: not
+      for (int c = threadIdx.x; c < n; c += ST) {
+        const unsigned long long w = wide[c];
+        keys[c * ks] = w > pre || (w == pre && c <= last);
+      }
+      cut = 1;
+      __syncthreads();
+    }
   }
-  if (need == 0) {
-    cut = ~0ull;
-    eq = 0;
-  }
-  // the chosen pages in order: every thread takes a run of pages
-  const int per = (n + ST - 1) / ST, c0 = min(n, (int)threadIdx.x * per), c1 = min(n, c0 + per);
-  uint2 mine = make_uint2(0, 0), all;
-  for (int c = c0; c < c1; ++c) {
-    mine.x += keys[c] > cut;
-    mine.y += keys[c] == cut;
-  }
-  const uint2 before = scan_pair(mine, warp_sums, &all);
-  int equal = (int)before.y, at = lo + (int)before.x + min(equal, eq);
-  for (int c = c0; c < c1; ++c) {
-    const bool take = keys[c] > cut || (keys[c] == cut && equal < eq);
-    equal += keys[c] == cut;
-    if (take) sel[at++] = lo + c;
+  // the chosen pages in order: 32 flags to a word, a word to a thread
+  if (need > 0) {
+    int done = lo;
+    for (int base = 0; base < n; base += ST * 32) {
+      for (int c0 = base; c0 < min(n, base + ST * 32); c0 += ST) {
+        const int c = c0 + threadIdx.x;
+        const unsigned word = __ballot_sync(0xffffffffu, c < n && keys[c * ks] >= cut);
+        if (lane == 0) bins[(c - base) >> 5] = (int)word;
+      }
+      __syncthreads();
+      const int words = (min(n - base, ST * 32) + ST - 1) / ST * (ST / 32);
+      unsigned word = (int)threadIdx.x < words ? (unsigned)bins[threadIdx.x] : 0u;
+      int total, at = done + scan_count(__popc(word), warp_sums, total);
+      for (; word; word &= word - 1) sel[at++] = lo + base + threadIdx.x * 32 + __ffs(word) - 1;
+      done += total;
+      __syncthreads();
+    }
   }
   for (int i = threadIdx.x; i < lo; i += ST) sel[i] = i;
   for (int i = threadIdx.x; i < p.keep_last; i += ST) sel[p.budget - p.keep_last + i] = held - p.keep_last + i;
@@ -544,12 +740,12 @@ cudaError_t launch_pages_write(const WriteParams &p, int dtype, int src_dtype, c
 }
 
 namespace {
-size_t select_smem(const PageGeom &g) { return g.width <= SELECT_SMEM_KEYS ? (size_t)g.width * 8 : 0; }
+size_t select_smem(const PageGeom &g) { return g.width <= SELECT_SMEM_KEYS ? (size_t)g.width * 4 : 0; }
 
 template <typename T, int D>
 cudaError_t select_attributes() {
   return cudaFuncSetAttribute(k_pages_select<T, D>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                              SELECT_SMEM_KEYS * 8);
+                              SELECT_SMEM_KEYS * 4);
 }
 
 template <typename T>
@@ -574,8 +770,6 @@ cudaError_t pages_init_attributes() {
   if (e == cudaSuccess) e = select_attributes<__half, 256>();
   return e;
 }
-
-bool pages_select_needs_keys(const PageGeom &g) { return g.width > SELECT_SMEM_KEYS; }
 
 cudaError_t launch_pages_select(const SelectParams &p, int dtype, cudaStream_t st) {
   return dtype == RTVLA_DTYPE_BF16 ? select<bf16>(p, st) : select<__half>(p, st);

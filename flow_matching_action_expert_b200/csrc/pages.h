@@ -75,10 +75,9 @@ struct SelectParams {
   const int32_t *lens;
   int budget, keep_first, keep_last;
   int32_t *sel;           // [batch][n_kv_heads][budget]
-  unsigned long long *keys;  // workspace [batch][n_kv_heads][width] of long tables, else null
+  unsigned long long *keys;  // workspace [batch][n_kv_heads][width]
   DevCtl *ctl;
 };
-bool pages_select_needs_keys(const PageGeom &g);
 cudaError_t launch_pages_select(const SelectParams &p, int dtype, cudaStream_t st);
 
 }  // namespace rtvla

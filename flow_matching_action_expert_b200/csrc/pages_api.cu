@@ -26,7 +26,7 @@ struct rtvla_pages_ctx {
   int *done = nullptr;  // plan: CTAs finished
   float *part_o = nullptr;
   float2 *part_ml = nullptr;
-  unsigned long long *keys = nullptr;  // select over long tables: [max_batch][n_kv_heads][table_width]
+  unsigned long long *keys = nullptr;  // select: [max_batch][n_kv_heads][table_width]
 };
 
 namespace {
@@ -129,7 +129,7 @@ rtvla_status p_create(rtvla_pages_ctx *c) {
   c->part_o = p_alloc<float>(c, parts * g.head_dim);
   c->part_ml = p_alloc<float2>(c, parts);
   if (!c->part_o || !c->part_ml) return RTVLA_ERR_OOM;
-  if (g.has_select && pages_select_needs_keys(c->g)) {
+  if (g.has_select) {
     c->keys = p_alloc<unsigned long long>(c, (size_t)g.max_batch * g.n_kv_heads * g.table_width);
     if (!c->keys) return RTVLA_ERR_OOM;
   }

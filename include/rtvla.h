@@ -469,8 +469,8 @@ typedef struct {
                        page_size < 2^32 - 1 */
   int table_width;  /* pages one request can hold; table_width * page_size <= 2^24 */
   int max_batch;    /* 1..4096 */
-  int has_select;   /* 1: rtvla_pages_select is used; a table_width above 8192 then takes a workspace of
-                       8 bytes per request, KV head and table entry */
+  int has_select;   /* 1: allocate rtvla_pages_select's workspace, 8 bytes per request, KV head and
+                       table entry */
   float rope_theta; /* RoPE base; 0: rtvla_pages_write does not rotate */
 } rtvla_pages_config;
 

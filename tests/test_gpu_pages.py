@@ -382,6 +382,38 @@ def test_select_with_equal_scores_and_extreme_ones():
     check_select(c, sel, 90, 0, 1)
 
 
+@pytest.mark.parametrize("page, tokens", [(1, 20000), (2, 70001)])
+def test_select_over_tables_longer_than_shared_memory(page, tokens):
+    c = Cache([tokens, 300, tokens - 77], d=64, hq=4, hkv=2, page=page)
+    m = c.k_mean[0]
+    m[c.table[2, 100:15000].long()] = 0.5  # thousands of equal scores around the cut
+    for budget in (100, 5000):
+        sel = torch.empty((3, 2, budget), dtype=torch.int32, device="cuda")
+        R.rtvla_pages_select(c.ctx, 0, c.q, c.kv, budget, 2, 3, sel)
+        assert c.status() == "RTVLA_OK"
+        check_select(c, sel, budget, 2, 3)
+
+
+def test_select_with_scores_closer_than_fp32_can_tell():
+    """Pages whose scores differ by less than an fp32 sum's rounding, and infinite ones."""
+    c = Cache([16 * 900, 16 * 900], page=16, d=128, hq=1)
+    rng = np.random.default_rng(11)
+    base = rng.normal(size=128).astype(np.float32) * 64
+    pages = c.table[0, :900].long()
+    m = torch.from_numpy(np.tile(base, (900, 1))).cuda().bfloat16()
+    m[:, 0] = torch.from_numpy(rng.integers(-3, 4, 900).astype(np.float32) * 2.0 ** -30).cuda().bfloat16()
+    c.k_mean[0, pages, 0] = m
+    pages = c.table[1, :900].long()
+    c.k_mean[0, pages[5:50:7], 0, 3] = float("inf")
+    c.k_mean[0, pages[6:800:7], 0, 3] = float("-inf")
+    c.q[1] = c.q[1].abs() + 0.125
+    for budget in (40, 400, 880):
+        sel = torch.empty((2, 1, budget), dtype=torch.int32, device="cuda")
+        R.rtvla_pages_select(c.ctx, 0, c.q, c.kv, budget, 0, 2, sel)
+        assert c.status() == "RTVLA_OK"
+        check_select(c, sel, budget, 0, 2)
+
+
 def test_select_puts_bad_pages_last_and_reports_them():
     c = Cache([16 * 40], d=64, hq=1, page=16)
     bad = c.table_np.copy()

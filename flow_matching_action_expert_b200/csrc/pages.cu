@@ -207,83 +207,188 @@ __global__ void __launch_bounds__(PT) k_pages_plan(PlanParams p) {
 namespace {
 size_t plan_smem(int batch) { return (size_t)(5 * batch + 3) * sizeof(int); }
 
+}  // namespace
+
 // ---------------------------------------------------------------------------------------
 // write
 
-// cos and sin of a position as the product of two table entries, e^{i(256 h + l)f} =
-// e^{i 256 h f} e^{i l f}: both tables hold fp64 angles rounded once, so the product is within
-// 2e-7 of the exact value at every position, and 2^24 positions need two tables of at most 2^16
-// rows instead of one of 2^24.
-__device__ __forceinline__ float2 rope_at(const float2 *lo, const float2 *hi, int pos, int i, int half) {
-  const float2 a = lo[(size_t)(pos & 255) * half + i], b = hi[(size_t)(pos >> 8) * half + i];
-  return make_float2(a.x * b.x - a.y * b.y, a.y * b.x + a.x * b.y);
+namespace {
+
+constexpr int WT = 256;       // threads of a write CTA
+constexpr int HEADS = 4;      // heads a thread moves: their loads are in flight together
+constexpr int MEAN_ROWS = 16; // rows a CTA searches for pages they fill
+
+// eight consecutive values as they lie in memory, and in fp32
+template <typename S>
+struct Raw8 {
+  uint4 v[sizeof(S) / 2];
+  __device__ __forceinline__ void load(const S *p) {
+#pragma unroll
+    for (int i = 0; i < (int)sizeof(S) / 2; ++i) v[i] = reinterpret_cast<const uint4 *>(p)[i];
+  }
+  __device__ __forceinline__ void to(float (&f)[8]) const {
+    const S *x = reinterpret_cast<const S *>(v);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) f[i] = to_f(x[i]);
+  }
+};
+template <typename S>
+__device__ __forceinline__ void load8(float (&f)[8], const S *p) {
+  Raw8<S> r;
+  r.load(p);
+  r.to(f);
+}
+template <typename T>
+__device__ __forceinline__ void store8(T *p, const float (&f)[8]) {
+  uint4 v;
+  T *x = reinterpret_cast<T *>(&v);
+#pragma unroll
+  for (int i = 0; i < 8; ++i) x[i] = from_f<T>(f[i]);
+  *reinterpret_cast<uint4 *>(p) = v;
+}
+
+// cos and sin of pairs 8 i8 .. 8 i8 + 7 at a position: the product of two table entries,
+// e^{i(256 h + l)f} = e^{i 256 h f} e^{i l f}.  Both tables hold fp64 angles rounded once, so the
+// product is within 2e-7 of the exact value at every position, and 2^24 positions need two tables
+// of at most 2^16 rows instead of one of 2^24.
+__device__ __forceinline__ void rope8(float (&c)[8], float (&s)[8], const WriteParams &p, int pos, int i8, int half) {
+  const float4 *lo = reinterpret_cast<const float4 *>(p.rope_lo + (size_t)(pos & 255) * half + i8 * 8);
+  const float4 *hi = reinterpret_cast<const float4 *>(p.rope_hi + (size_t)(pos >> 8) * half + i8 * 8);
+#pragma unroll
+  for (int u = 0; u < 4; ++u) {
+    const float4 a = lo[u], b = hi[u];
+    c[2 * u] = a.x * b.x - a.y * b.y;
+    s[2 * u] = a.y * b.x + a.x * b.y;
+    c[2 * u + 1] = a.z * b.z - a.w * b.w;
+    s[2 * u + 1] = a.w * b.z + a.z * b.w;
+  }
+}
+__device__ __forceinline__ void rotate8(float (&x1)[8], float (&x2)[8], const float (&c)[8], const float (&s)[8]) {
+#pragma unroll
+  for (int u = 0; u < 8; ++u) {
+    const float y = x1[u] * c[u] - x2[u] * s[u];
+    x2[u] = x2[u] * c[u] + x1[u] * s[u];
+    x1[u] = y;
+  }
 }
 
 }  // namespace
 
-// One CTA per row.
+// Moves bytes: a row is read once and written once, with two table rows of 8 bytes per pair that
+// its heads share through L1.  A thread takes eight pairs (16 bytes of each half) of HEADS heads.
+// The first CTAs look for rows that fill their page.  The mean of such a page needs the rows of this
+// call that other CTAs write, so it is computed from their sources again; the page's earlier keys
+// come from the pool.
 template <typename T, typename S>
-__global__ void __launch_bounds__(128) k_pages_write(WriteParams p) {
+__global__ void __launch_bounds__(WT) k_pages_write(WriteParams p, int mean_ctas) {
   const PageGeom g = p.g;
-  const int r = blockIdx.x, d = g.head_dim, half = d / 2;
-  const int hq = p.n_q_heads, hkv = g.n_kv_heads, ld = (hq + 2 * hkv) * d;
-  bool bad = false;
-  const int slot = pg_slot(p.slots[r], g, &bad), pos = p.positions[r];
-  if (slot >= 0 && (pos < 0 || pos >= g.width << g.shift)) bad = true;
-  if (bad && threadIdx.x == 0) set_error(p.ctl, DEVERR_BOUNDS, PG_AT_WRITE);
-  if (slot < 0 || bad) return;
+  const int d = g.head_dim, half = d / 2, blocks = d / 16;  // blocks of eight pairs
+  const int hq = p.n_q_heads, hkv = g.n_kv_heads, heads = hq + 2 * hkv, cap = g.width << g.shift;
+  const size_t ld = (size_t)heads * d;
   const S *src = static_cast<const S *>(p.qkv);
   T *k = static_cast<T *>(p.k), *v = static_cast<T *>(p.v), *q = static_cast<T *>(p.q_out);
-  // the rotated, rounded pair i of head h of row `row` at position `at`
-  auto pair = [&](int row, int at, int h, int i, T &y1, T &y2) {
-    const S *x = src + (size_t)row * ld + h * d;
-    const float x1 = to_f(x[i]), x2 = to_f(x[i + half]);
-    const float2 cs = p.rope_lo ? rope_at(p.rope_lo, p.rope_hi, at, i, half) : make_float2(1.f, 0.f);
-    y1 = from_f<T>(x1 * cs.x - x2 * cs.y);
-    y2 = from_f<T>(x2 * cs.x + x1 * cs.y);
-  };
-  for (int u = threadIdx.x; u < (hq + hkv) * half; u += blockDim.x) {
-    const int h = u / half, i = u % half;
-    T y1, y2;
-    pair(r, pos, h, i, y1, y2);
-    T *dst = h < hq ? q + (size_t)r * hq * d + h * d : k + pg_elem(p.layer, slot, h - hq, g);
-    dst[i] = y1;
-    dst[i + half] = y2;
-  }
-  for (int u = threadIdx.x; u < hkv * d; u += blockDim.x)
-    v[pg_elem(p.layer, slot, u / d, g) + u % d] = from_f<T>(to_f(src[(size_t)r * ld + (hq + hkv) * d + u]));
-  const int ps = 1 << g.shift;
-  if (!p.k_mean || (slot & (ps - 1)) != ps - 1) return;
-  // this row fills its page: its keys are this call's rows r, r - 1, ... as far as their slots run
-  // on downwards (other CTAs write those, so they are computed again here), and the pool's below
-  __shared__ int run;
-  if (threadIdx.x == 0) run = min(ps, r + 1);
-  __syncthreads();
-  for (int i = threadIdx.x; i < min(ps, r + 1); i += blockDim.x)
-    if (p.slots[r - i] != slot - i) atomicMin(&run, i);
-  __syncthreads();
-  const int from = ps - run;
-  T *mean = static_cast<T *>(p.k_mean);
-  for (int u = threadIdx.x; u < hkv * half; u += blockDim.x) {
-    const int h = u / half, i = u % half;
-    float s1 = 0.f, s2 = 0.f;
-    for (int o = 0; o < ps; ++o) {
-      T y1, y2;
-      if (o < from) {
-        const T *x = k + pg_elem(p.layer, slot - (ps - 1) + o, h, g);
-        y1 = x[i];
-        y2 = x[i + half];
-      } else {
-        const int row = r - (ps - 1 - o);
-        const int at = min(max(p.positions[row], 0), (g.width << g.shift) - 1);
-        pair(row, at, hq + h, i, y1, y2);
-      }
-      s1 += to_f(y1);
-      s2 += to_f(y2);
+  if ((int)blockIdx.x >= mean_ctas) {
+    const int groups = (heads + HEADS - 1) / HEADS;
+    const uint32_t item = (blockIdx.x - mean_ctas) * (uint32_t)WT + threadIdx.x;  // at least 32 bytes of qkv each
+    const uint32_t at = item / (uint32_t)blocks, r = at / (uint32_t)groups;
+    const int i8 = (int)(item % (uint32_t)blocks), h0 = (int)(at - r * groups);  // heads h0, h0 + groups, ...
+    if (r >= (uint32_t)p.n_rows) return;
+    // the row's values are requested before its slot is known
+    const int want = p.slots[r], pos = p.positions[r];
+    Raw8<S> raw1[HEADS], raw2[HEADS];
+#pragma unroll
+    for (int u = 0; u < HEADS; ++u) {
+      const S *x = src + r * ld + (size_t)min(h0 + u * groups, heads - 1) * d + i8 * 8;
+      raw1[u].load(x);
+      raw2[u].load(x + half);
     }
-    T *dst = mean + pg_mean_elem(p.layer, slot >> g.shift, h, g);
-    dst[i] = from_f<T>(s1 / ps);
-    dst[i + half] = from_f<T>(s2 / ps);
+    bool bad = false;
+    const int slot = pg_slot(want, g, &bad);
+    if (slot >= 0 && (pos < 0 || pos >= cap)) bad = true;
+    if (bad) set_error(p.ctl, DEVERR_BOUNDS, PG_AT_WRITE);
+    if (slot < 0 || bad) return;
+    float c[8], s[8];
+    if (p.rope_lo) rope8(c, s, p, pos, i8, half);
+#pragma unroll
+    for (int u = 0; u < HEADS; ++u) {
+      const int h = h0 + u * groups;
+      if (h >= heads) break;
+      float x1[8], x2[8];
+      raw1[u].to(x1);
+      raw2[u].to(x2);
+      if (p.rope_lo && h < hq + hkv) rotate8(x1, x2, c, s);
+      T *dst = h < hq ? q + ((size_t)r * hq + h) * d
+                      : h < hq + hkv ? k + pg_elem(p.layer, slot, h - hq, g)
+                                     : v + pg_elem(p.layer, slot, h - hq - hkv, g);
+      store8(dst + i8 * 8, x1);
+      store8(dst + i8 * 8 + half, x2);
+    }
+    return;
+  }
+  // ---- page means
+  __shared__ float sums[WT * 16];  // [WT / blocks][d]
+  __shared__ int run;
+  const int ps = 1 << g.shift, i8 = threadIdx.x % blocks, lane_r = threadIdx.x / blocks, n_lanes = WT / blocks;
+  const int r0 = (int)blockIdx.x * MEAN_ROWS;
+  // every warp looks at all the rows of this CTA, a row per lane
+  const int lane = threadIdx.x & 31, my_r = r0 + lane;
+  int my_slot = -1;
+  if (lane < MEAN_ROWS && my_r < p.n_rows) {
+    bool bad = false;
+    my_slot = pg_slot(p.slots[my_r], g, &bad);
+    const int at = p.positions[my_r];
+    if (at < 0 || at >= cap || (my_slot & (ps - 1)) != ps - 1) my_slot = -1;
+  }
+  for (unsigned fills = __ballot_sync(0xffffffffu, my_slot >= 0); fills; fills &= fills - 1) {
+    const int i = __ffs(fills) - 1, r = r0 + i, slot = __shfl_sync(0xffffffffu, my_slot, i);
+    // rows r, r - 1, ... fill the page downwards as far as their slots run on
+    const int most = min(ps, r + 1);
+    __syncthreads();
+    if (threadIdx.x == 0) run = most;
+    __syncthreads();
+    for (int i = threadIdx.x; i < most; i += WT)
+      if (p.slots[r - i] != slot - i) atomicMin(&run, i);
+    __syncthreads();
+    const int from = ps - run;
+    for (int h = 0; h < hkv; ++h) {
+      float a1[8] = {0, 0, 0, 0, 0, 0, 0, 0}, a2[8] = {0, 0, 0, 0, 0, 0, 0, 0};
+#pragma unroll 2
+      for (int o = lane_r; o < ps; o += n_lanes) {
+        float x1[8], x2[8];
+        if (o < from) {
+          const T *x = k + pg_elem(p.layer, slot - (ps - 1) + o, h, g) + i8 * 8;
+          load8(x1, x);
+          load8(x2, x + half);
+        } else {
+          const int row = r - (ps - 1 - o), pos = min(max(p.positions[row], 0), cap - 1);
+          const S *x = src + row * ld + (size_t)(hq + h) * d + i8 * 8;
+          load8(x1, x);
+          load8(x2, x + half);
+          if (p.rope_lo) {
+            float c[8], s[8];
+            rope8(c, s, p, pos, i8, half);
+            rotate8(x1, x2, c, s);
+          }
+        }
+#pragma unroll
+        for (int u = 0; u < 8; ++u) {  // keys as stored
+          a1[u] += to_f(from_f<T>(x1[u]));
+          a2[u] += to_f(from_f<T>(x2[u]));
+        }
+      }
+#pragma unroll
+      for (int u = 0; u < 8; ++u) {
+        sums[lane_r * d + i8 * 8 + u] = a1[u];
+        sums[lane_r * d + half + i8 * 8 + u] = a2[u];
+      }
+      __syncthreads();
+      for (int i = threadIdx.x; i < d; i += WT) {
+        float sum = 0.f;
+        for (int l = 0; l < min(n_lanes, ps); ++l) sum += sums[l * d + i];
+        static_cast<T *>(p.k_mean)[pg_mean_elem(p.layer, slot >> g.shift, h, g) + i] = from_f<T>(sum / ps);
+      }
+      __syncthreads();
+    }
   }
 }
 
@@ -727,16 +832,23 @@ cudaError_t launch_pages_plan(const PlanParams &p, int sm_count, cudaStream_t st
   return cudaGetLastError();
 }
 
+namespace {
+template <typename T, typename S>
+cudaError_t write(const WriteParams &p, cudaStream_t st) {
+  const int heads = p.n_q_heads + 2 * p.g.n_kv_heads;
+  const long long items = (long long)p.n_rows * ((heads + HEADS - 1) / HEADS) * (p.g.head_dim / 16);
+  const long long move = (items + WT - 1) / WT;
+  const int mean = p.k_mean ? (p.n_rows + MEAN_ROWS - 1) / MEAN_ROWS : 0;
+  k_pages_write<T, S><<<(unsigned)(move + mean), WT, 0, st>>>(p, mean);
+  return cudaGetLastError();
+}
+}  // namespace
+
 cudaError_t launch_pages_write(const WriteParams &p, int dtype, int src_dtype, cudaStream_t st) {
   if (p.n_rows == 0) return cudaSuccess;
-  if (dtype == RTVLA_DTYPE_BF16) {
-    if (src_dtype == RTVLA_DTYPE_F32) k_pages_write<bf16, float><<<p.n_rows, 128, 0, st>>>(p);
-    else k_pages_write<bf16, bf16><<<p.n_rows, 128, 0, st>>>(p);
-  } else {
-    if (src_dtype == RTVLA_DTYPE_F32) k_pages_write<__half, float><<<p.n_rows, 128, 0, st>>>(p);
-    else k_pages_write<__half, __half><<<p.n_rows, 128, 0, st>>>(p);
-  }
-  return cudaGetLastError();
+  const bool f32 = src_dtype == RTVLA_DTYPE_F32;
+  if (dtype == RTVLA_DTYPE_BF16) return f32 ? write<bf16, float>(p, st) : write<bf16, bf16>(p, st);
+  return f32 ? write<__half, float>(p, st) : write<__half, __half>(p, st);
 }
 
 namespace {

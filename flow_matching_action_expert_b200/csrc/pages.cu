@@ -28,9 +28,8 @@ __device__ __forceinline__ __half from_f<__half>(float v) { return __float2half_
 // ---------------------------------------------------------------------------------------
 // plan
 
-constexpr int PT = 256;  // threads of the plan kernel
-
-// Exclusive scan of one value per thread over the block; *total receives the sum.
+// Exclusive scan of one value per thread over a block of PT; *total receives the sum.
+template <int PT>
 __device__ long long block_scan(long long v, long long *total, long long *warp_sums) {
   const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
   long long inc = v;
@@ -42,14 +41,15 @@ __device__ long long block_scan(long long v, long long *total, long long *warp_s
   __syncthreads();  // warp_sums free again
   if (lane == 31) warp_sums[w] = inc;
   __syncthreads();
-  long long before = 0, all = 0;
+  long long sums = lane < PT / 32 ? warp_sums[lane] : 0;
 #pragma unroll
-  for (int i = 0; i < PT / 32; ++i) {
-    if (i < w) before += warp_sums[i];
-    all += warp_sums[i];
+  for (int o = 1; o < 32; o <<= 1) {
+    const long long n = __shfl_up_sync(0xffffffffu, sums, o);
+    if (lane >= o) sums += n;
   }
-  *total = all;
-  return before + inc - v;
+  const long long before = __shfl_sync(0xffffffffu, sums, (w + 31) & 31);
+  *total = __shfl_sync(0xffffffffu, sums, 31);
+  return (w ? before : 0) + inc - v;
 }
 
 // Last index b with cum[b] <= i (cum[0] = 0, i < cum[n]): the request that owns item i.
@@ -74,6 +74,7 @@ __device__ __forceinline__ int owner(const int *cum, int n, int i) {
 // A decode step is one CTA: a chain of two scans and three dependent loads.  With more rows every
 // CTA repeats the scans and takes a share of the rows and pages; the last one to finish writes the
 // lengths and the new top, which the others still read (they may be updated in place).
+template <int PT>
 __global__ void __launch_bounds__(PT) k_pages_plan(PlanParams p) {
   extern __shared__ int sm[];
   __shared__ long long warp_sums[PT / 32];
@@ -99,7 +100,7 @@ __global__ void __launch_bounds__(PT) k_pages_plan(PlanParams p) {
 
   long long sum = 0, total;
   for (int b = b0; b < b1; ++b) sum += max(s_delta[b], 0);
-  long long rows = block_scan(sum, &total, warp_sums);
+  long long rows = block_scan<PT>(sum, &total, warp_sums);
   if (threadIdx.x == 0) s_rows[B] = (int)min(total, (long long)p.n_rows);
   long long take = 0, back = 0;
   for (int b = b0; b < b1; ++b) {
@@ -120,8 +121,8 @@ __global__ void __launch_bounds__(PT) k_pages_plan(PlanParams p) {
     }
   }
   long long all_take, all_back;
-  take = block_scan(take, &all_take, warp_sums);
-  back = block_scan(back, &all_back, warp_sums);
+  take = block_scan<PT>(take, &all_take, warp_sums);
+  back = block_scan<PT>(back, &all_back, warp_sums);
   const int nf = min(max(raw_free, 0), g.n_pages);
   // a table that gives back more pages than the pool has is the caller's fault
   const int n_back = (int)min(all_back, (long long)(g.n_pages - nf));
@@ -826,9 +827,14 @@ __global__ void __cluster_dims__(SC, 1, 1) __launch_bounds__(ST, 2) k_pages_sele
 // launchers
 
 cudaError_t launch_pages_plan(const PlanParams &p, int sm_count, cudaStream_t st) {
-  // four rows per thread: the scans cost every CTA about 4 us, as much as a thread's four rows
-  const int want = (p.n_rows + 4 * PT - 1) / (4 * PT);
-  k_pages_plan<<<want < 1 ? 1 : want < sm_count ? want : sm_count, PT, plan_smem(p.batch), st>>>(p);
+  // A CTA's time is the scans over the requests: 1024 threads from 256 requests on (2000 requests:
+  // PLAN_NOTE).  Two rows per thread: every CTA repeats the scans, so more of them only
+  // help until each SM has one.
+  const bool many = p.batch > 256;
+  const int threads = many ? 1024 : 256, want = (p.n_rows + 2 * threads - 1) / (2 * threads);
+  const int ctas = want < 1 ? 1 : want < sm_count ? want : sm_count;
+  if (many) k_pages_plan<1024><<<ctas, threads, plan_smem(p.batch), st>>>(p);
+  else k_pages_plan<256><<<ctas, threads, plan_smem(p.batch), st>>>(p);
   return cudaGetLastError();
 }
 
@@ -873,7 +879,7 @@ cudaError_t select(const SelectParams &p, cudaStream_t st) {
 
 cudaError_t pages_init_attributes() {
   cudaError_t e =
-      cudaFuncSetAttribute(k_pages_plan, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)plan_smem(4096));
+      cudaFuncSetAttribute(k_pages_plan<1024>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)plan_smem(4096));
   if (e == cudaSuccess) e = select_attributes<bf16, 64>();
   if (e == cudaSuccess) e = select_attributes<bf16, 128>();
   if (e == cudaSuccess) e = select_attributes<bf16, 256>();

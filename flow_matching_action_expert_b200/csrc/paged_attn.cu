@@ -465,6 +465,18 @@ __global__ void __launch_bounds__(JOIN_THREADS) k_pages_join(PagedAttnParams p, 
   auto part = [&](int i) {  // the i-th part's place in the workspace
     return ((size_t)(from + i) * 2 + (i == 0 ? second : 0)) * G + head;
   };
+  // eight loads in flight, the first ones before the weights are known
+  const int col = threadIdx.x % COLS, row = threadIdx.x / COLS;
+  float4 x[8];
+  auto load = [&](int i0) {
+#pragma unroll
+    for (int u = 0; u < 8; ++u) {
+      const int i = i0 + u * ROWS;
+      x[u] = i < parts ? *reinterpret_cast<const float4 *>(p.part_o + part(i) * D + d0 + col * 4)
+                       : make_float4(0.f, 0.f, 0.f, 0.f);
+    }
+  };
+  load(row);
   // weight of every part: 2^(m_i - M) / sum_i 2^(m_i - M) l_i
   float M = -INFINITY;
   for (int i = threadIdx.x; i < parts; i += JOIN_THREADS) {
@@ -491,16 +503,8 @@ __global__ void __launch_bounds__(JOIN_THREADS) k_pages_join(PagedAttnParams p, 
   L = 0.f;
 #pragma unroll
   for (int w = 0; w < JOIN_THREADS / 32; ++w) L += red_s[1][w];
-  const int col = threadIdx.x % COLS, row = threadIdx.x / COLS;
   float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-  for (int i0 = row; i0 < parts; i0 += 8 * ROWS) {  // eight loads in flight
-    float4 x[8];
-#pragma unroll
-    for (int u = 0; u < 8; ++u) {
-      const int i = i0 + u * ROWS;
-      x[u] = i < parts ? *reinterpret_cast<const float4 *>(p.part_o + part(i) * D + d0 + col * 4)
-                       : make_float4(0.f, 0.f, 0.f, 0.f);
-    }
+  for (int i0 = row; i0 < parts;) {
 #pragma unroll
     for (int u = 0; u < 8; ++u) {
       const float f = i0 + u * ROWS < parts ? part_s[i0 + u * ROWS].x : 0.f;
@@ -509,6 +513,8 @@ __global__ void __launch_bounds__(JOIN_THREADS) k_pages_join(PagedAttnParams p, 
       v.z += f * x[u].z;
       v.w += f * x[u].w;
     }
+    i0 += 8 * ROWS;
+    if (i0 < parts) load(i0);
   }
   acc_s[row][col] = v;
   __syncthreads();

@@ -33,7 +33,7 @@ EXPORTS = (
     "rtvla_vision_create", "rtvla_encode_images", "rtvla_vision_debug_trace", "rtvla_vision_sync_status",
     "rtvla_vision_kernels_per_call", "rtvla_vision_destroy",
     "rtvla_pages_create", "rtvla_pages_plan", "rtvla_pages_write", "rtvla_pages_attend", "rtvla_pages_select",
-    "rtvla_pages_sync_status", "rtvla_pages_destroy",
+    "rtvla_pages_sync_status", "rtvla_pages_destroy", "rtvla_prefix_step",
 )
 
 
@@ -141,6 +141,7 @@ def _lib():
         lib.rtvla_pages_attend.argtypes = [_P, ctypes.c_int, _P, _KV, _P, ctypes.c_int, _P, _P]
         lib.rtvla_pages_select.argtypes = [_P, ctypes.c_int, _P, _KV, ctypes.c_int, ctypes.c_int, ctypes.c_int, _P,
                                            _P]
+        lib.rtvla_prefix_step.argtypes = [_P, _P, _P, _P, _P, _KV, _P, _P]
         lib.rtvla_pages_sync_status.argtypes = [_P, _P]
         lib.rtvla_pages_destroy.argtypes = [_P]
         lib.rtvla_pages_destroy.restype = None
@@ -408,6 +409,11 @@ def rtvla_pages_select(ctx: int, layer: int, q, kv: RtvlaPagedKV, budget: int, k
                        stream=None):
     _check(_lib().rtvla_pages_select(ctx, layer, _ptr(q), ctypes.byref(kv), budget, keep_first, keep_last, _ptr(sel),
                                      _stream(stream)), "rtvla_pages_select")
+
+
+def rtvla_prefix_step(ctx: int, pages: int, embeds, slots, positions, kv: RtvlaPagedKV, hidden, stream=None):
+    _check(_lib().rtvla_prefix_step(ctx, pages, _ptr(embeds), _ptr(slots), _ptr(positions), ctypes.byref(kv),
+                                    _ptr(hidden), _stream(stream)), "rtvla_prefix_step")
 
 
 def rtvla_pages_sync_status(ctx: int, stream=None) -> int:

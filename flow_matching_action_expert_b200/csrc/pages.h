@@ -6,6 +6,7 @@
 
 #include "common.cuh"
 #include "pages_index.h"
+#include "rtvla.h"
 
 namespace rtvla {
 
@@ -79,5 +80,10 @@ struct SelectParams {
   DevCtl *ctl;
 };
 cudaError_t launch_pages_select(const SelectParams &p, int dtype, cudaStream_t st);
+
+// Checks a call that uses a context as the prefix model's cache (defined beside the C ABI).
+rtvla_status pages_check_prefix(const rtvla_pages_ctx *c, int device, int n_layers, int n_q_heads, int head_dim,
+                                float rope_theta, const int32_t *slots, const int32_t *positions,
+                                const rtvla_paged_kv *kv);
 
 }  // namespace rtvla

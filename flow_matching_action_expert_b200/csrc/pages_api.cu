@@ -169,6 +169,21 @@ rtvla_status launched(cudaError_t e) {
 
 }  // namespace
 
+namespace rtvla {
+rtvla_status pages_check_prefix(const rtvla_pages_ctx *c, int device, int n_layers, int n_q_heads, int head_dim,
+                                float rope_theta, const int32_t *slots, const int32_t *positions,
+                                const rtvla_paged_kv *kv) {
+  const rtvla_pages_config &g = c->cfg;
+  if (c->device != device || g.dtype != RTVLA_DTYPE_BF16 || g.n_layers != n_layers || g.n_q_heads != n_q_heads ||
+      g.n_kv_heads != 1 || g.head_dim != head_dim || g.rope_theta != rope_theta)
+    return RTVLA_ERR_UNSUPPORTED;
+  const rtvla_status s = check_kv(c, 0, kv);
+  if (s != RTVLA_OK) return s;
+  if (!aligned(slots, 4) || !aligned(positions, 4)) return RTVLA_ERR_INVALID_ARG;
+  return check_requests(c, kv);
+}
+}  // namespace rtvla
+
 // =======================================================================================
 // C ABI
 

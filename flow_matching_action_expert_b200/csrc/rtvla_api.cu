@@ -21,6 +21,7 @@
 
 #include "common.cuh"
 #include "kernels.h"
+#include "pages.h"
 #include "persistent.h"
 #include "rtvla.h"
 
@@ -1136,6 +1137,63 @@ rtvla_status rtvla_prefill(rtvla_ctx *c, const void *prefix_embeds, const uint8_
   if (cudaMemcpyAsync(c->args_pf, &a, sizeof(a), cudaMemcpyHostToDevice, st) != cudaSuccess) return RTVLA_ERR_CUDA;
   if (cudaGraphLaunch(it->second.exec, st) != cudaSuccess) return RTVLA_ERR_CUDA;
   return RTVLA_OK;
+}
+
+static rtvla_status prefix_step(rtvla_ctx *c, rtvla_pages_ctx *pages, const void *embeds, const int32_t *slots,
+                                const int32_t *positions, const rtvla_paged_kv *kv, float *hidden, cudaStream_t st) {
+#define CKS(x)                                    \
+  do {                                            \
+    if ((x) != cudaSuccess) {                     \
+      cudaGetLastError();                         \
+      return RTVLA_ERR_CUDA;                      \
+    }                                             \
+  } while (0)
+  const int M = kv->batch;
+  const float eps = c->cfg.rms_eps;
+  const bool glu = gemm_glu_applies(M, FP, DP, c->sm_count);
+  // the accumulator starts at zero for both GEMMs that use it
+  CKS(cudaMemsetAsync(c->pacc, 0, (size_t)M * (glu ? 2560 : 2 * FP) * 4, st));
+  CKS(launch_scale_to_f32(static_cast<const bf16 *>(embeds), M * DP, 1.0, c->px, st));
+  for (int l = 0; l < c->L; ++l) {
+    CKS(launch_rmsnorm(c->px, c->pop, M, DP, eps, st));
+    CKS(gemm_launch(c->tm_pwqkv, l * 2560, c->tm_pop, M, 2560, DP, c->pacc, c->tmo_pqkv, 2560, nullptr, false, c->ctl,
+                    c->sm_count, st));
+    rtvla_status s = rtvla_pages_write(pages, l, c->pacc, RTVLA_DTYPE_F32, slots, positions, M, kv, c->pq, st);
+    if (s == RTVLA_OK) s = rtvla_pages_attend(pages, l, c->pq, kv, nullptr, 0, c->po, st);
+    if (s != RTVLA_OK) return s;
+    CKS(cudaMemsetAsync(c->pacc, 0, (size_t)M * 2560 * 4, st));
+    CKS(gemm_launch(c->tm_pwo, l * DP, c->tm_po, M, DP, NQH * HD, c->px, c->tmo_px, DP, nullptr, true, c->ctl,
+                    c->sm_count, st));
+    CKS(launch_rmsnorm(c->px, c->pop, M, DP, eps, st));
+    if (glu) {
+      CKS(gemm_launch_glu(c->tm_pwgu64, l * 2 * FP, c->tm_pop, M, FP, DP, c->tm_pmb.m[0], nullptr, nullptr, c->ctl,
+                          c->sm_count, st));
+    } else {
+      CKS(gemm_launch(c->tm_pwgu, l * 2 * FP, c->tm_pop, M, 2 * FP, DP, c->pacc, c->tmo_pgu, 2 * FP, nullptr, false,
+                      c->ctl, c->sm_count, st));
+      CKS(launch_gelu_mul(c->pacc, nullptr, nullptr, c->pmb, M, FP, st));
+    }
+    CKS(gemm_launch(c->tm_pwd, l * DP, c->tm_pmb, M, DP, FP, c->px, c->tmo_px, DP, nullptr, true, c->ctl, c->sm_count, st));
+  }
+  CKS(cudaMemcpyAsync(hidden, c->px, (size_t)M * DP * 4, cudaMemcpyDeviceToDevice, st));
+#undef CKS
+  return RTVLA_OK;
+}
+
+rtvla_status rtvla_prefix_step(rtvla_ctx *c, rtvla_pages_ctx *pages, const void *embeds, const int32_t *slots,
+                               const int32_t *positions, const rtvla_paged_kv *kv, float *hidden, void *stream) {
+  if (!c || !pages || !embeds || !slots || !positions || !kv || !hidden || kv->batch < 1) return RTVLA_ERR_INVALID_ARG;
+  if (!c->cfg.has_prefill) return RTVLA_ERR_UNSUPPORTED;
+  rtvla_status s =
+      pages_check_prefix(pages, c->device, c->L, NQH, HD, c->cfg.rope_theta, slots, positions, kv);
+  if (s != RTVLA_OK) return s;
+  if (kv->batch > c->Bmax) return RTVLA_ERR_SHAPE;
+  int device = -1;
+  if (cudaGetDevice(&device) != cudaSuccess || (device != c->device && cudaSetDevice(c->device) != cudaSuccess))
+    return RTVLA_ERR_CUDA;
+  s = prefix_step(c, pages, embeds, slots, positions, kv, hidden, static_cast<cudaStream_t>(stream));
+  if (device != c->device) cudaSetDevice(device);
+  return s;
 }
 
 rtvla_status rtvla_sync_status(rtvla_ctx *c, void *stream) {

@@ -559,6 +559,24 @@ rtvla_status rtvla_pages_attend(rtvla_pages_ctx *ctx, int layer, const void *q, 
 rtvla_status rtvla_pages_select(rtvla_pages_ctx *ctx, int layer, const void *q, const rtvla_paged_kv *kv,
                                 int budget, int keep_first, int keep_last, int32_t *sel, void *stream);
 
+/*
+ * The prefix pass for one new token per request, on a paged cache: embeds, device bf16
+ * [kv->batch][pf_width] (scaled as rtvla_prefill's), run through all layers of the prefix model.
+ * In every layer the token's K and V are written to slots[b] (slots, positions: as
+ * rtvla_pages_plan gives them for one new token per request; kv->lens counts it already), and it
+ * attends to the kv->lens[b] tokens its request holds: rtvla_prefill's layer for one query, which
+ * sees what came before it and itself.  hidden: device f32 [kv->batch][pf_width], the residual
+ * stream after the last layer (the final norm and a vocabulary's product are the caller's).  The
+ * row of a request whose slot is -1 is unspecified.  ctx needs has_prefill; pages needs ctx's
+ * n_layers, 8 query heads and 1 KV head of 256, bf16 and ctx's rope_theta, and it reports the
+ * device errors of its part.  On a pool that is an rtvla_kv the cache can go on to
+ * rtvla_sample_actions.  Launches kernels directly, so that it can be captured; it must not overlap
+ * another call on ctx or on pages.  Errors: INVALID_ARG, SHAPE (batch > max_batch of either),
+ * UNSUPPORTED, CUDA.
+ */
+rtvla_status rtvla_prefix_step(rtvla_ctx *ctx, rtvla_pages_ctx *pages, const void *embeds, const int32_t *slots,
+                               const int32_t *positions, const rtvla_paged_kv *kv, float *hidden, void *stream);
+
 /* As rtvla_sync_status, for a paged-cache context (NO_PAGES, DEVICE_BOUNDS, GUARD_OVERWRITE). */
 rtvla_status rtvla_pages_sync_status(rtvla_pages_ctx *ctx, void *stream);
 

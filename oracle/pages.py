@@ -10,6 +10,8 @@ from __future__ import annotations
 
 import numpy as np
 
+from . import model as _model
+
 
 def pages_for(n: int, page: int) -> int:
     return -(-n // page)
@@ -116,3 +118,24 @@ def choose(score, held, budget, keep_first, keep_last):
     lo, hi = keep_first, held - keep_last
     best = sorted(range(lo, hi), key=lambda e: (-score[e], e))[: budget - keep_first - keep_last]
     return sorted(list(range(lo)) + best + list(range(hi, held)))
+
+
+def prefix_step(weights, cfg, embed, K, V, pos):
+    """One token through the prefix model: embed [Dp]; K, V: per layer the n keys and values held,
+    [n][hd].  Returns (hidden [Dp] after the last layer, the token's keys [L][hd], values [L][hd]).
+
+    The layer of oracle/model.py's prefix pass, for one query that sees every token held and itself.
+    """
+    x, ks, vs = np.asarray(embed, np.float64), [], []
+    for l in range(cfg.n_layers):
+        W = {n: np.asarray(weights[f"pf{l}.{n}"], np.float64)
+             for n in ("ln1", "wq", "wk", "wv", "wo", "ln2", "wg", "wu", "wd")}
+        n1 = _model.rms_normalize(x, cfg.rms_eps) * (1.0 + W["ln1"])
+        q = rope((W["wq"] @ n1).reshape(cfg.n_q_heads, cfg.head_dim), pos, cfg.rope_theta)
+        ks.append(rope(W["wk"] @ n1, pos, cfg.rope_theta))
+        vs.append(W["wv"] @ n1)
+        o = attend_one(q, np.vstack([K[l], ks[-1]]), np.vstack([V[l], vs[-1]]))[0]
+        x = x + W["wo"] @ o.reshape(-1)
+        n2 = _model.rms_normalize(x, cfg.rms_eps) * (1.0 + W["ln2"])
+        x = x + W["wd"] @ (_model.gelu_tanh(W["wg"] @ n2) * (W["wu"] @ n2))
+    return x, np.array(ks), np.array(vs)

@@ -71,6 +71,22 @@ def test_rope_is_the_prefix_models_rotation():
     assert np.abs(got - O.rope(x, pos, 10000.0)).max() < 1e-10
 
 
+def test_prefix_step_is_the_prefix_pass_of_the_last_token():
+    """Layer 0's keys and values do not depend on the mask, so the last of n tokens gets from a step
+    what it gets from the whole pass: its keys of layer 1 and, alone in its cache, everything."""
+    from oracle import model as O
+    from synth import workloads as WL
+    shape = WL.PrefillShape(n_layers=2, width=64, mlp_dim=96, n_q_heads=4, n_kv_heads=1, head_dim=16)
+    W = {k: v * 8 for k, v in WL.as_f32(WL.prefill_weights(shape)).items()}
+    x = np.random.default_rng(13).normal(size=(1, 7, 64)) * 8
+    K, V, _ = O.prefill(W, shape, x, np.ones((1, 7), np.uint8))
+    _, k, v = OP.prefix_step(W, shape, x[0, 6], K[:, 0, :6], V[:, 0, :6], 6)
+    assert np.abs(k - K[:, 0, 6]).max() < 1e-11 and np.abs(v - V[:, 0, 6]).max() < 1e-11
+    K, V, _ = O.prefill(W, shape, x[:, :1], np.ones((1, 1), np.uint8))
+    _, k, v = OP.prefix_step(W, shape, x[0, 0], np.zeros((2, 0, 16)), np.zeros((2, 0, 16)), 0)
+    assert np.abs(k - K[:, 0, 0]).max() < 1e-11 and np.abs(v - V[:, 0, 0]).max() < 1e-11
+
+
 def test_choice_keeps_first_and_last_and_breaks_ties_low():
     s = np.array([9., 1., 5., 5., 5., 2., 8., 0.])
     assert OP.choose(s, 8, 8, 1, 1) == list(range(8))
@@ -174,6 +190,7 @@ def test_null_arguments_are_refused():
                  lib.rtvla_pages_write(None, 0, None, 0, None, None, 0, ref, None, None),
                  lib.rtvla_pages_attend(None, 0, None, ref, None, 0, None, None),
                  lib.rtvla_pages_select(None, 0, None, ref, 1, 0, 1, None, None),
+                 lib.rtvla_prefix_step(None, None, None, None, None, ref, None, None),
                  lib.rtvla_pages_sync_status(None, None)):
         assert R.STATUS[code] == "RTVLA_ERR_INVALID_ARG"
     R.rtvla_pages_destroy(0)

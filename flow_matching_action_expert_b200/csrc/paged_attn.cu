@@ -130,7 +130,9 @@ __global__ void __launch_bounds__(WARPS * 32, ctas_per_sm<D, NT>()) k_pages_atte
   const PageGeom g = p.g;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, gq = lane >> 2, t4 = lane & 3;
   const int G = p.n_q_heads / g.n_kv_heads, B = p.batch;
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  // Launched while the kernel before it may still run (rtvla_pages_write and _select let it), so
+  // nothing is read before this; the join is launched likewise.
+  asm volatile("griddepcontrol.wait;\n\tgriddepcontrol.launch_dependents;" ::: "memory");
 
   // this CTA's range of chunks, and the request it starts in
   const int per = (B + WARPS * 32 - 1) / (WARPS * 32);
@@ -543,22 +545,25 @@ cudaError_t attend(const PagedAttnParams &p, int sm_count, cudaStream_t st) {
   const long long most = (long long)p.batch * p.g.n_kv_heads * ((keys + CHUNK - 1) / CHUNK);
   const long long wave = std::min(sm_count * ctas_per_sm<D, NT>(), MAX_CTAS);
   const int ctas = (int)(most < wave ? most : wave);
-  k_pages_attend<T, D, NT><<<ctas, WARPS * 32, Smem<D, NT>::TOTAL, st>>>(p);
-  const cudaError_t e = cudaGetLastError();
+  cudaLaunchAttribute attr;
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(ctas);
+  cfg.blockDim = dim3(WARPS * 32);
+  cfg.dynamicSmemBytes = Smem<D, NT>::TOTAL;
+  cfg.stream = st;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, k_pages_attend<T, D, NT>, p);
   if (e != cudaSuccess) return e;
   // Few (request, head) pairs have many parts each and take 512 threads; many pairs have few parts,
   // and most of their CTAs only find that there is nothing to do: smaller ones pass faster (24 x 32
   // pairs: 64.2 us with 256 threads, 71.2 with 512; one pair of 148 parts: 49.0 and 36.7 us).
-  cudaLaunchAttribute attr;
-  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr.val.programmaticStreamSerializationAllowed = 1;
   const bool few = (long long)p.n_q_heads * p.batch * (D / 64) <= sm_count;
-  cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(p.n_q_heads * (few ? D / 64 : 1), p.batch);
   cfg.blockDim = dim3(few ? 512 : 256);
-  cfg.stream = st;
-  cfg.attrs = &attr;
-  cfg.numAttrs = 1;
+  cfg.dynamicSmemBytes = 0;
   return few ? cudaLaunchKernelEx(&cfg, k_pages_join<T, D, 512, 64>, p, ctas)
              : cudaLaunchKernelEx(&cfg, k_pages_join<T, D, 256, D>, p, ctas);
 }

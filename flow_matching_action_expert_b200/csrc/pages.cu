@@ -288,6 +288,7 @@ __global__ void __launch_bounds__(WT) k_pages_write(WriteParams p, int mean_ctas
   const size_t ld = (size_t)heads * d;
   const S *src = static_cast<const S *>(p.qkv);
   T *k = static_cast<T *>(p.k), *v = static_cast<T *>(p.v), *q = static_cast<T *>(p.q_out);
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");  // the attention may be launched
   if ((int)blockIdx.x >= mean_ctas) {
     const int groups = (heads + HEADS - 1) / HEADS;
     const uint32_t item = (blockIdx.x - mean_ctas) * (uint32_t)WT + threadIdx.x;  // at least 32 bytes of qkv each
@@ -490,6 +491,7 @@ __global__ void __cluster_dims__(SC, 1, 1) __launch_bounds__(ST, 2) k_pages_sele
   const PageGeom g = p.g;
   const int rank = blockIdx.x, h = blockIdx.y, b = blockIdx.z, G = p.n_q_heads / g.n_kv_heads;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");  // the attention may be launched
   constexpr int LPP = D / 8, PPW = 32 / LPP;  // lanes per page, pages per load
   const int sub = lane / LPP, ln = lane % LPP;
   // the sum of the group's query heads, one component per thread; loads that need no length first

@@ -32,6 +32,7 @@ namespace {
 
 constexpr int WARPS = 4;
 constexpr int CHUNK = 64;  // keys per unit of work: one 16-key tile per warp
+constexpr int SETUP = 1;   // units that starting a pair and joining its warps count in the split
 constexpr int SLOTS = 3;   // ring of a warp: tiles of 16 rows, K and V in turn
 constexpr int MAX_CTAS = 1024;  // of one launch
 
@@ -79,11 +80,13 @@ __device__ __forceinline__ void copy_wait() {
   asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
 
-// chunks of request b (of each of its KV heads)
-__device__ __forceinline__ int chunks_of(const PagedAttnParams &p, int b) {
+// units of work of request b (of each of its KV heads): its chunks, behind SETUP units for what
+// every pair costs besides
+__device__ __forceinline__ int units_of(const PagedAttnParams &p, int b) {
   bool bad = false;
   const int len = pg_len(p.lens[b], p.g, &bad);
-  return (pg_list_len(len, p.sel_width, p.sel != nullptr, p.g) + CHUNK - 1) / CHUNK;
+  const int n = pg_list_len(len, p.sel_width, p.sel != nullptr, p.g);
+  return n > 0 ? (n + CHUNK - 1) / CHUNK + SETUP : 0;
 }
 
 // a / b (a >= 0, b > 0), in 32 bits where they suffice: a 64-bit division takes a hundred
@@ -134,13 +137,13 @@ __global__ void __launch_bounds__(WARPS * 32, ctas_per_sm<D, NT>()) k_pages_atte
   // nothing is read before this; the join is launched likewise.
   asm volatile("griddepcontrol.wait;\n\tgriddepcontrol.launch_dependents;" ::: "memory");
 
-  // this CTA's range of chunks, and the request it starts in
+  // this CTA's range of units, and the request it starts in
   const int per = (B + WARPS * 32 - 1) / (WARPS * 32);
   const int b0 = min(B, (int)threadIdx.x * per), b1 = min(B, b0 + per);
   long long mine = 0;
   bool bad = false;
   for (int b = b0; b < b1; ++b) {
-    mine += chunks_of(p, b);
+    mine += units_of(p, b);
     if (blockIdx.x == 0) pg_len(p.lens[b], g, &bad);
   }
   if (bad) set_error(p.ctl, DEVERR_BOUNDS, PG_AT_ATTEND);
@@ -170,7 +173,7 @@ __global__ void __launch_bounds__(WARPS * 32, ctas_per_sm<D, NT>()) k_pages_atte
   if (before <= start && start < before + mine * g.n_kv_heads) {
     int b = b0;
     for (; b < b1 - 1; ++b) {
-      const long long n = (long long)chunks_of(p, b) * g.n_kv_heads;
+      const long long n = (long long)units_of(p, b) * g.n_kv_heads;
       if (start < before + n) break;
       before += n;
     }
@@ -178,10 +181,9 @@ __global__ void __launch_bounds__(WARPS * 32, ctas_per_sm<D, NT>()) k_pages_atte
     first_at = start - before;
   }
   __syncthreads();
-  int b = first_b, n_chunks = max(chunks_of(p, b), 1);
-  int h = min((int)quotient(first_at, n_chunks), g.n_kv_heads - 1), c0 = (int)(first_at - (long long)h * n_chunks);
-  long long left = end - start;
-  bool at_start = true;
+  int b = first_b, n_units = max(units_of(p, b), 1);
+  int h = min((int)quotient(first_at, n_units), g.n_kv_heads - 1), u0 = (int)(first_at - (long long)h * n_units);
+  long long at = start;  // unit of the whole work
 
   uint8_t *ring = smem + warp * S::RING;
   const uint32_t ring_a = smem_u32(ring), q_a = smem_u32(smem + WARPS * S::RING);
@@ -189,7 +191,9 @@ __global__ void __launch_bounds__(WARPS * 32, ctas_per_sm<D, NT>()) k_pages_atte
 
   while (true) {
     // ---- one segment: chunks [c0, c1) of (b, h)
-    const int c1 = (int)min((long long)n_chunks, c0 + left);
+    const int u1 = (int)min((long long)n_units, u0 + (end - at));
+    const int c0 = max(u0 - SETUP, 0), c1 = u1 - SETUP, n_chunks = n_units - SETUP;
+    if (c1 > c0) {
     const int len = pg_len(p.lens[b], g, &bad);
     const int n = pg_list_len(len, p.sel_width, p.sel != nullptr, g);
     const int32_t *trow = p.table + (size_t)b * g.width;
@@ -355,7 +359,8 @@ __global__ void __launch_bounds__(WARPS * 32, ctas_per_sm<D, NT>()) k_pages_atte
       }
     __syncthreads();
     const bool whole = c0 == 0 && c1 == n_chunks;
-    const size_t part = (size_t)blockIdx.x * 2 + (at_start ? 0 : 1);
+    // a CTA's parts: of a pair that began before it, and of one that goes on after it
+    const size_t part = (size_t)blockIdx.x * 2 + (c0 == 0 ? 1 : 0);
     for (int i = threadIdx.x; i < G * (D / 4); i += WARPS * 32) {
       const int head = i / (D / 4), d = (i % (D / 4)) * 4;
       float M = -INFINITY, L = 0.f;
@@ -387,20 +392,20 @@ __global__ void __launch_bounds__(WARPS * 32, ctas_per_sm<D, NT>()) k_pages_atte
       }
     }
 
-    left -= c1 - c0;
-    if (left == 0) break;
+    }
+    at += u1 - u0;
+    if (at >= end) break;
     __syncthreads();
-    at_start = false;
-    c0 = 0;
+    u0 = 0;
     if (++h == g.n_kv_heads) {  // the next request that holds anything
       h = 0;
       for (++b; b < B; b += 32) {
-        const int c = b + lane < B ? chunks_of(p, b + lane) : 0;
+        const int c = b + lane < B ? units_of(p, b + lane) : 0;
         const unsigned some = __ballot_sync(0xffffffffu, c > 0);
         if (some) {
-          const int at = __ffs(some) - 1;
-          n_chunks = __shfl_sync(0xffffffffu, c, at);
-          b += at;
+          const int to = __ffs(some) - 1;
+          n_units = __shfl_sync(0xffffffffu, c, to);
+          b += to;
           break;
         }
       }
@@ -427,7 +432,7 @@ __global__ void __launch_bounds__(JOIN_THREADS) k_pages_join(PagedAttnParams p, 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   long long before = 0, total = 0;
   for (int i = threadIdx.x; i < p.batch; i += JOIN_THREADS) {
-    const long long c = chunks_of(p, i);
+    const long long c = units_of(p, i);
     total += c;
     if (i < b) before += c;
   }
@@ -447,13 +452,13 @@ __global__ void __launch_bounds__(JOIN_THREADS) k_pages_join(PagedAttnParams p, 
     before += sum_s[0][w];
     total += sum_s[1][w];
   }
-  const long long n = chunks_of(p, b);
+  const long long n = units_of(p, b);
   T *out = static_cast<T *>(p.out) + ((size_t)b * p.n_q_heads + hq) * D + d0;
   total *= g.n_kv_heads;
   const long long x0 = before * g.n_kv_heads + n * h, x1 = x0 + n;
   const long long ctas = max(min(total, (long long)grid), 1ll);
-  // chunk x belongs to the CTA c with total c / ctas <= x < total (c + 1) / ctas
-  const int from = n ? (int)quotient((x0 + 1) * ctas - 1, total) : 0, to = n ? (int)quotient(x1 * ctas - 1, total) : 0;
+  // unit x belongs to the CTA c with total c / ctas <= x < total (c + 1) / ctas
+  const int from = n ? (int)quotient((x0 + SETUP + 1) * ctas - 1, total) : 0, to = n ? (int)quotient(x1 * ctas - 1, total) : 0;
   asm volatile("griddepcontrol.wait;" ::: "memory");
   if (n == 0) {
     for (int i = threadIdx.x; i < W; i += JOIN_THREADS) put(out + i, 0.f);
@@ -462,10 +467,8 @@ __global__ void __launch_bounds__(JOIN_THREADS) k_pages_join(PagedAttnParams p, 
   const int parts = to - from + 1;
   if (parts == 1) return;  // finished where it was computed
   const int head = hq - h * G;
-  // a CTA's second part if the pair begins inside the CTA's range: only the first one can
-  const int second = quotient(total * from, ctas) < x0 ? 1 : 0;
   auto part = [&](int i) {  // the i-th part's place in the workspace
-    return ((size_t)(from + i) * 2 + (i == 0 ? second : 0)) * G + head;
+    return ((size_t)(from + i) * 2 + (i == 0 ? 1 : 0)) * G + head;
   };
   // eight loads in flight, the first ones before the weights are known
   const int col = threadIdx.x % COLS, row = threadIdx.x / COLS;
@@ -540,9 +543,9 @@ namespace {
 
 template <typename T, int D, int NT>
 cudaError_t attend(const PagedAttnParams &p, int sm_count, cudaStream_t st) {
-  // one wave of CTAs, but no more than there can be chunks
+  // one wave of CTAs, but no more than there can be units
   const long long keys = (long long)(p.sel && p.sel_width < p.g.width ? p.sel_width : p.g.width) << p.g.shift;
-  const long long most = (long long)p.batch * p.g.n_kv_heads * ((keys + CHUNK - 1) / CHUNK);
+  const long long most = (long long)p.batch * p.g.n_kv_heads * ((keys + CHUNK - 1) / CHUNK + SETUP);
   const long long wave = std::min(sm_count * ctas_per_sm<D, NT>(), MAX_CTAS);
   const int ctas = (int)(most < wave ? most : wave);
   cudaLaunchAttribute attr;

@@ -546,8 +546,10 @@ __global__ void __cluster_dims__(SC, 1, 1) __launch_bounds__(ST, 2) k_pages_sele
         bad = true;
         mine = -1;
       }
-      // the page's number among all layers' and heads' means; page 0 in place of a missing one
-      const uint32_t mean_at = ((uint32_t)p.layer * g.n_pages + (uint32_t)max(mine, 0)) * g.n_kv_heads + h;
+      // the page's number among all layers' and heads' means; in place of a missing one the run's first
+      // (its score is not used, but what is read takes part in the bound)
+      const int first = max(__shfl_sync(0xffffffffu, mine, 0), 0), there = mine >= 0 ? mine : first;
+      const uint32_t mean_at = ((uint32_t)p.layer * g.n_pages + (uint32_t)there) * g.n_kv_heads + h;
       constexpr int LOADS = LPP / 2 < 8 ? LPP / 2 : 8, STEP = LOADS * PPW;  // loads in flight, their pages
       static_assert(RUN % STEP == 0, "whole steps");
 #pragma unroll

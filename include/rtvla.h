@@ -510,7 +510,8 @@ rtvla_status rtvla_pages_create(const rtvla_pages_config *cfg, rtvla_pages_ctx *
  * table_width pages or rows past n_rows refuse that request alone and report DEVICE_BOUNDS; a page
  * number outside the pool (in the table or the free list) gives its rows slot -1 and reports the
  * same.  row_start counts every request's rows, refused ones too, up to n_rows.
- * n_rows 0..2^24; slots and positions may be null when it is 0.  Errors: INVALID_ARG, SHAPE, CUDA.
+ * A page may appear in several requests' tables (a shared prompt), but a request that shrinks must
+ * not share what it gives back.  n_rows 0..2^24; slots and positions may be null when it is 0.  Errors: INVALID_ARG, SHAPE, CUDA.
  */
 rtvla_status rtvla_pages_plan(rtvla_pages_ctx *ctx, const int32_t *lens, const int32_t *delta,
                               int32_t *free_pages, const int32_t *n_free, const rtvla_paged_kv *kv,
@@ -524,8 +525,8 @@ rtvla_status rtvla_pages_plan(rtvla_pages_ctx *ctx, const int32_t *lens, const i
  * q_out, device [n_rows][n_q_heads * head_dim].  Rows with slot -1 are skipped: nothing of theirs
  * is written.  A row whose token is the last of its page also writes that page's k_mean (when not
  * null): the mean, summed in fp32, of the page's keys as stored.  A page's earlier tokens must be
- * in the pool already or in this call's rows directly before; slots must be distinct.  Reads
- * kv->k, v, k_mean only.  A slot or position outside the cache skips its row and reports
+ * in the pool already or in this call's rows directly before; slots must be distinct, and q_out
+ * must not overlap qkv.  Uses kv->k, v and k_mean only.  A slot or position outside the cache skips its row and reports
  * DEVICE_BOUNDS.  Errors: INVALID_ARG (null, misaligned, n_rows < 0), SHAPE, CUDA.
  */
 rtvla_status rtvla_pages_write(rtvla_pages_ctx *ctx, int layer, const void *qkv, int qkv_dtype,
@@ -538,7 +539,8 @@ rtvla_status rtvla_pages_write(rtvla_pages_ctx *ctx, int layer, const void *qkv,
  * where it holds none.  q, out: device [batch][n_q_heads][head_dim] of the cache's dtype, 16-byte
  * aligned.  sel, if not null: device int32 [batch][n_kv_heads][sel_width], the logical pages
  * (0 .. pages held - 1) to attend to instead of all, the first min(sel_width, pages held) entries
- * used; a page listed twice counts twice.  Sums, maxima and weights are fp32.  A length past the
+ * used; a page listed twice counts twice.  Sums, maxima and weights are fp32; an infinite value
+ * among those attended to gives NaN.  Nothing past a request's length is read.  A length past the
  * table is clamped; keys of a page number outside the pool, or of a listed page that is not held,
  * are left out; each reports DEVICE_BOUNDS.  Errors: INVALID_ARG, SHAPE, CUDA.
  */

@@ -1,17 +1,6 @@
 """The paged KV cache on the GPU (rtvla_pages_*), against the fp64 oracle.
 
-Tolerances, with u = eps / 2 of the output's type (one rounding) and e = 2^-24 (fp32):
-  attend  a logit is a d-term fp32 sum of exact products, times a rounded scale: off by at most
-          D = (d + 4) e S, S = max_j sum_i |q_i k_ji| / sqrt(d).  A weight exp(s) / sum is off by a
-          relative 2 D (numerator and sum) + 8 e (two exponentials of 2 ulp each way, one division)
-          + (n + 64) e (the fp32 sums over n keys, joined); weights split into two 16-bit halves
-          add 2^-16.  With A = sum_j p_j |v_j|:  |out - ref| <= u |ref| + (2 D + (2 n + 136) e + 2^-16) A.
-          An f16 output below 2^-14 rounds in steps of 2^-24: + 2^-25.  f16 halves of a weight round
-          in steps of 2^-24 of the largest weight: + n 2^-25 max |v| for f16.
-  write   cos and sin of a table product are within 4 e, two products and a sum add 3 e:
-          |y - ref| <= u |ref| + 7 e (|x1| + |x2|); values are rounded once.
-  k_mean  against the stored keys: u |ref| + page e mean|k|.
-  plan, select: equal.
+Tolerances: tests/pages_tolerances.py.  Plans and selections are equal.
 """
 import numpy as np
 import pytest
@@ -20,9 +9,10 @@ import torch
 import flow_matching_action_expert_b200 as R
 from oracle import pages as OP
 
+from pages_tolerances import E32, attend_tolerance
+
 pytestmark = pytest.mark.gpu
 
-E32 = 2.0 ** -24
 TYPES = {"bf16": (torch.bfloat16, R.DTYPE_BF16), "f16": (torch.float16, R.DTYPE_F16)}
 
 
@@ -98,13 +88,10 @@ class Cache:
                 self.close(got[b, h * G:(h + 1) * G], ref, size, big, kk, vv, (b, h, n))
 
     def close(self, got, ref, size, big, kk, vv, what):
-        m = len(kk)
-        tol = self.u * np.abs(ref) + (2 * (self.d + 4) * E32 * big + (2 * m + 136) * E32 + 2.0 ** -16) * size
-        if self.f16:
-            tol += 2.0 ** -25 * (1 + m * np.abs(vv).max() if m else 1)
+        tol = attend_tolerance(self.u, self.d, self.f16, ref, size, big, vv)
         err = np.abs(got - ref)
         assert np.isfinite(got).all() and (err <= tol).all(), (what, float((err - tol).max()))
-        if m == 0:
+        if len(kk) == 0:
             assert not got.any()
 
 

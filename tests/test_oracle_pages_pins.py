@@ -63,6 +63,34 @@ def test_attention_matches_torch_on_shuffled_pages():
     assert not OP.attend_one(q, np.zeros((0, d)), np.zeros((0, d)))[0].any()
 
 
+@pytest.mark.parametrize("mistake", ["last key missing", "one key too many", "scale", "heads swapped", "page off by one",
+                                     "value of the next key"])
+@pytest.mark.parametrize("u, f16", [(2.0 ** -8, False), (2.0 ** -11, True)])
+def test_planted_mistakes_leave_the_attention_tolerance(mistake, u, f16):
+    """Each mistake, made in the oracle, lands outside the bound the GPU tests use on 200 keys."""
+    from pages_tolerances import attend_tolerance
+    rng = np.random.default_rng(17)
+    d, n, page, G = 128, 200, 16, 4
+    k, v = rng.normal(size=(2, 20, 1, page, d))
+    row, q = rng.permutation(20)[:13], rng.normal(size=(G, d))
+    kk, vv = OP.keys_of(k, row, n, 0, page), OP.keys_of(v, row, n, 0, page)
+    ref, size, big = OP.attend_one(q, kk, vv)
+    if mistake == "last key missing":
+        bad = OP.attend_one(q, kk[:-1], vv[:-1])[0]
+    elif mistake == "one key too many":
+        bad = OP.attend_one(q, OP.keys_of(k, row, n + 1, 0, page), OP.keys_of(v, row, n + 1, 0, page))[0]
+    elif mistake == "scale":
+        bad = OP.attend_one(q * d ** -0.5, kk, vv)[0]
+    elif mistake == "heads swapped":
+        bad = OP.attend_one(q[::-1], kk, vv)[0]
+    elif mistake == "page off by one":
+        bad = OP.attend_one(q, OP.keys_of(k, (row + 1) % 20, n, 0, page), vv)[0]
+    else:
+        bad = OP.attend_one(q, kk, np.roll(vv, -1, 0))[0]
+    tol = attend_tolerance(u, d, f16, ref, size, big, vv)
+    assert (np.abs(bad - ref) > tol).mean() > 0.1
+
+
 def test_rope_is_the_prefix_models_rotation():
     from oracle import model as O
     x = np.random.default_rng(9).normal(size=(5, 256))

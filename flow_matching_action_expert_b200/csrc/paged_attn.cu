@@ -7,9 +7,18 @@
 // components of d as M.  (A tcgen05 tile has M >= 64 and its operands in one shared buffer per
 // CTA; with 8 query rows it would only add barriers.)
 //
-// One warp owns a 16-key tile and a private ring of stages filled by cp.async, so that nothing in
-// the main loop waits for another warp; each warp keeps its own running maximum, sum and O^T in
-// registers.  At the end of a request's keys the four warps' results are joined in shared memory.
+// One warp owns a 16-key tile and a private ring filled by cp.async, K and V tiles in turn, so that
+// nothing in the main loop waits for another warp; each warp keeps its own running maximum, sum and
+// O^T in registers.  At the end of a request's keys the four warps' results are joined in shared
+// memory.  Three tiles per warp and two CTAs per SM (d = 256) keep 128 KB per SM in flight; three
+// pairs of tiles and one CTA per SM keep as much but leave an SM idle at the end of each request
+// (16 requests of 800 tokens: 13.8 us, with two CTAs 11.8; 64 of up to 32768: 178.7 and 181.3).
+//
+// Measured: 64 requests of up to 32768 tokens, 8 heads of 256 on one KV head (1.13 GB of K and V),
+// 181 us, 6.26 TB/s, 95% of the GPU's measured copy rate; 24 ragged requests, 32/8 heads of 128 in
+// f16 (351 MB) 65 us, 5.4 TB/s; one request of 131071 tokens (134 MB) 33 us, of which the reading
+// takes 21 and the start, the last tiles and the join the rest.  Short calls are latency: 8.3 us
+// for one request of 544 tokens.
 //
 // The work is split evenly whatever the lengths: the 64-key chunks of all (request, KV head)
 // pairs, in order, are cut into one contiguous range per CTA.  A pair that lies inside one range is

@@ -592,26 +592,30 @@ cudaError_t attend(const PagedAttnParams &p, int sm_count, cudaStream_t st) {
 }
 
 template <typename T, int D>
-cudaError_t allow_smem() {
-  const cudaError_t e = cudaFuncSetAttribute(k_pages_attend<T, D, 1>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                             Smem<D, 1>::TOTAL);
-  return e != cudaSuccess ? e
-                          : cudaFuncSetAttribute(k_pages_attend<T, D, 2>,
-                                                 cudaFuncAttributeMaxDynamicSharedMemorySize, Smem<D, 2>::TOTAL);
+cudaError_t allow_smem(int group) {
+  return group <= 8 ? cudaFuncSetAttribute(k_pages_attend<T, D, 1>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                           Smem<D, 1>::TOTAL)
+                    : cudaFuncSetAttribute(k_pages_attend<T, D, 2>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                           Smem<D, 2>::TOTAL);
+}
+
+template <typename T>
+cudaError_t allow_smem(int head_dim, int group) {
+  if (head_dim == 64) return allow_smem<T, 64>(group);
+  return head_dim == 128 ? allow_smem<T, 128>(group) : allow_smem<T, 256>(group);
 }
 
 }  // namespace
 
-int pages_attend_parts(int sm_count) { return 2 * std::min(4 * sm_count, MAX_CTAS); }
+int pages_attend_parts(int head_dim, int group, int sm_count) {
+  int ctas;
+  if (group <= 8) ctas = head_dim == 64 ? ctas_per_sm<64, 1>() : head_dim == 128 ? ctas_per_sm<128, 1>() : ctas_per_sm<256, 1>();
+  else ctas = head_dim == 64 ? ctas_per_sm<64, 2>() : head_dim == 128 ? ctas_per_sm<128, 2>() : ctas_per_sm<256, 2>();
+  return 2 * std::min(ctas * sm_count, MAX_CTAS);
+}
 
-cudaError_t pages_attend_init_attributes() {
-  cudaError_t e = allow_smem<bf16, 64>();
-  if (e == cudaSuccess) e = allow_smem<bf16, 128>();
-  if (e == cudaSuccess) e = allow_smem<bf16, 256>();
-  if (e == cudaSuccess) e = allow_smem<__half, 64>();
-  if (e == cudaSuccess) e = allow_smem<__half, 128>();
-  if (e == cudaSuccess) e = allow_smem<__half, 256>();
-  return e;
+cudaError_t pages_attend_init_attributes(int dtype, int head_dim, int group) {
+  return dtype == RTVLA_DTYPE_BF16 ? allow_smem<bf16>(head_dim, group) : allow_smem<__half>(head_dim, group);
 }
 
 cudaError_t launch_pages_attend(const PagedAttnParams &p, int dtype, int sm_count, cudaStream_t st) {

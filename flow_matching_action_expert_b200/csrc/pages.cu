@@ -839,6 +839,23 @@ __global__ void __cluster_dims__(SC, 1, 1) __launch_bounds__(ST, 2) k_pages_sele
 // ---------------------------------------------------------------------------------------
 // launchers
 
+namespace {
+// (cos, sin) of positions step * row, angle = position * theta^(-2 i / d) in fp64, rounded once
+__global__ void k_rope_table(float2 *dst, int rows, int step, int half, double theta) {
+  const size_t n = (size_t)rows * half;
+  for (size_t at = (size_t)blockIdx.x * blockDim.x + threadIdx.x; at < n; at += (size_t)gridDim.x * blockDim.x) {
+    double s, c;
+    sincos((double)(at / half) * step * pow(theta, -(double)(at % half) / half), &s, &c);
+    dst[at] = make_float2((float)c, (float)s);
+  }
+}
+}  // namespace
+
+cudaError_t launch_rope_table(float2 *dst, int rows, int step, int head_dim, double theta, cudaStream_t st) {
+  k_rope_table<<<592, 256, 0, st>>>(dst, rows, step, head_dim / 2, theta);
+  return cudaGetLastError();
+}
+
 cudaError_t launch_pages_plan(const PlanParams &p, int sm_count, cudaStream_t st) {
   // A CTA's time is the scans over the requests: 1024 threads from 256 requests on (2000 requests and
   // 91 thousand rows: 13.9 us, with 256 threads 17.1).  Two rows per thread: every CTA repeats the scans, so more of them only
@@ -873,10 +890,10 @@ cudaError_t launch_pages_write(const WriteParams &p, int dtype, int src_dtype, c
 namespace {
 size_t select_smem(const PageGeom &g) { return g.width <= SELECT_SMEM_KEYS ? (size_t)g.width * 4 : 0; }
 
-template <typename T, int D>
-cudaError_t select_attributes() {
-  return cudaFuncSetAttribute(k_pages_select<T, D>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                              SELECT_SMEM_KEYS * 4);
+template <typename T>
+cudaError_t select_attributes(int head_dim) {
+  const auto kernel = head_dim == 64 ? k_pages_select<T, 64> : head_dim == 128 ? k_pages_select<T, 128> : k_pages_select<T, 256>;
+  return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, SELECT_SMEM_KEYS * 4);
 }
 
 template <typename T>
@@ -890,16 +907,11 @@ cudaError_t select(const SelectParams &p, cudaStream_t st) {
 }
 }  // namespace
 
-cudaError_t pages_init_attributes() {
-  cudaError_t e =
+cudaError_t pages_init_attributes(int dtype, int head_dim) {
+  const cudaError_t e =
       cudaFuncSetAttribute(k_pages_plan<1024>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)plan_smem(4096));
-  if (e == cudaSuccess) e = select_attributes<bf16, 64>();
-  if (e == cudaSuccess) e = select_attributes<bf16, 128>();
-  if (e == cudaSuccess) e = select_attributes<bf16, 256>();
-  if (e == cudaSuccess) e = select_attributes<__half, 64>();
-  if (e == cudaSuccess) e = select_attributes<__half, 128>();
-  if (e == cudaSuccess) e = select_attributes<__half, 256>();
-  return e;
+  if (e != cudaSuccess) return e;
+  return dtype == RTVLA_DTYPE_BF16 ? select_attributes<bf16>(head_dim) : select_attributes<__half>(head_dim);
 }
 
 cudaError_t launch_pages_select(const SelectParams &p, int dtype, cudaStream_t st) {

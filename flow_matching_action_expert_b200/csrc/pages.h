@@ -30,7 +30,8 @@ struct PlanParams {
   int *done;  // workspace: CTAs finished, 0 between calls
   DevCtl *ctl;
 };
-cudaError_t pages_init_attributes();
+cudaError_t pages_init_attributes(int dtype, int head_dim);
+cudaError_t launch_rope_table(float2 *dst, int rows, int step, int head_dim, double theta, cudaStream_t st);
 cudaError_t launch_pages_plan(const PlanParams &p, int sm_count, cudaStream_t st);
 
 struct WriteParams {
@@ -63,8 +64,8 @@ struct PagedAttnParams {
   float2 *part_ml;        // workspace [parts][group]: their maximum (log2 units) and sum
   DevCtl *ctl;
 };
-int pages_attend_parts(int sm_count);  // parts the workspace holds
-cudaError_t pages_attend_init_attributes();
+int pages_attend_parts(int head_dim, int group, int sm_count);  // parts the workspace holds
+cudaError_t pages_attend_init_attributes(int dtype, int head_dim, int group);
 cudaError_t launch_pages_attend(const PagedAttnParams &p, int dtype, int sm_count, cudaStream_t st);
 
 struct SelectParams {

@@ -2,7 +2,6 @@
 // and workspaces, and the launches.
 #include <cmath>
 #include <cstdlib>
-#include <cstring>
 #include <new>
 #include <vector>
 
@@ -16,8 +15,8 @@ struct rtvla_pages_ctx {
   rtvla_pages_config cfg;
   PageGeom g;
   int device = 0, sm_count = 148;
-  std::vector<void *> allocs;
-  size_t mem_cap = 0, mem_used = 0;
+  unsigned char *arena = nullptr;  // one allocation holds every buffer
+  size_t mem_cap = 0;
   bool checked = false;
   std::vector<GuardRegion> guards;
   GuardRegion *d_guards = nullptr;
@@ -43,34 +42,26 @@ struct OnDevice {
   }
 };
 
-// Allocation with the context's memory cap and, in checked mode, guard bands (as the denoise
-// context's buffers).
-template <typename T>
-T *p_alloc(rtvla_pages_ctx *c, size_t n) {
-  void *p = nullptr;
-  const size_t bytes = (n * sizeof(T) + 255) & ~size_t(255);
-  const size_t total = c->checked ? bytes + 2 * (size_t)GUARD_BYTES : bytes;
-  if (c->mem_cap && c->mem_used + total > c->mem_cap) return nullptr;
-  if (cudaMalloc(&p, total) != cudaSuccess) {
-    cudaGetLastError();
-    return nullptr;
+// Hands out 256-byte aligned buffers of an arena (of a null one, to find its size).  In checked mode
+// each lies between two guard bands, as the denoise context's buffers do.
+struct Carve {
+  rtvla_pages_ctx *c;
+  unsigned char *base;
+  size_t at = 0;
+  template <typename T>
+  void operator()(T *&p, size_t n) {
+    const size_t bytes = (n * sizeof(T) + 255) & ~size_t(255);
+    if (c->checked) {
+      if (base) c->guards.push_back(GuardRegion{base + at, (unsigned long long)bytes});
+      at += GUARD_BYTES;
+    }
+    if (base) p = reinterpret_cast<T *>(base + at);
+    at += bytes + (c->checked ? GUARD_BYTES : 0);
   }
-  c->allocs.push_back(p);
-  c->mem_used += total;
-  if (!c->checked) return static_cast<T *>(p);
-  unsigned char *b = static_cast<unsigned char *>(p);
-  if (cudaMemset(b, GUARD_FILL, GUARD_BYTES) != cudaSuccess ||
-      cudaMemset(b + GUARD_BYTES + bytes, GUARD_FILL, GUARD_BYTES) != cudaSuccess) {
-    cudaGetLastError();
-    return nullptr;
-  }
-  c->guards.push_back(GuardRegion{b, (unsigned long long)bytes});
-  return reinterpret_cast<T *>(b + GUARD_BYTES);
-}
+};
 
 void p_free(rtvla_pages_ctx *c) {
-  for (void *p : c->allocs) cudaFree(p);
-  if (c->d_guards) cudaFree(c->d_guards);
+  if (c->arena) cudaFree(c->arena);
   delete c;
 }
 
@@ -91,57 +82,53 @@ rtvla_status check_cfg(const rtvla_pages_config *g) {
   return RTVLA_OK;
 }
 
-// (cos, sin) of positions step * i, angle = position * theta^(-2j/d) in fp64, rounded once
-rtvla_status build_rope(float2 *dst, int rows, int step, int d, double theta) {
-  std::vector<float2> t((size_t)rows * (d / 2));
-  std::vector<double> freq(d / 2);
-  for (int j = 0; j < d / 2; ++j) freq[j] = std::pow(theta, -2.0 * j / d);
-  for (int i = 0; i < rows; ++i)
-    for (int j = 0; j < d / 2; ++j) {
-      const double a = (double)i * step * freq[j];
-      t[(size_t)i * (d / 2) + j] = make_float2((float)std::cos(a), (float)std::sin(a));
-    }
-  return cudaMemcpy(dst, t.data(), t.size() * sizeof(float2), cudaMemcpyHostToDevice) == cudaSuccess
-             ? RTVLA_OK
-             : RTVLA_ERR_CUDA;
-}
-
 rtvla_status p_create(rtvla_pages_ctx *c) {
   const rtvla_pages_config &g = c->cfg;
   if (cudaGetDevice(&c->device) != cudaSuccess ||
       cudaDeviceGetAttribute(&c->sm_count, cudaDevAttrMultiProcessorCount, c->device) != cudaSuccess)
     return RTVLA_ERR_CUDA;
-  if (pages_init_attributes() != cudaSuccess || pages_attend_init_attributes() != cudaSuccess) return RTVLA_ERR_CUDA;
-  c->ctl = p_alloc<DevCtl>(c, 1);
-  c->done = p_alloc<int>(c, 1);
-  if (!c->ctl || !c->done) return RTVLA_ERR_OOM;
-  if (cudaMemset(c->done, 0, sizeof(int)) != cudaSuccess) return RTVLA_ERR_CUDA;
-  if (g.rope_theta > 0.f) {
-    const int hi = ((g.table_width * g.page_size - 1) >> 8) + 1;
-    c->rope_lo = p_alloc<float2>(c, (size_t)256 * (g.head_dim / 2));
-    c->rope_hi = p_alloc<float2>(c, (size_t)hi * (g.head_dim / 2));
-    if (!c->rope_lo || !c->rope_hi) return RTVLA_ERR_OOM;
-    if (build_rope(c->rope_lo, 256, 1, g.head_dim, g.rope_theta) != RTVLA_OK ||
-        build_rope(c->rope_hi, hi, 256, g.head_dim, g.rope_theta) != RTVLA_OK)
-      return RTVLA_ERR_CUDA;
+  const int group = g.n_q_heads / g.n_kv_heads;
+  if (pages_init_attributes(g.dtype, g.head_dim) != cudaSuccess ||
+      pages_attend_init_attributes(g.dtype, g.head_dim, group) != cudaSuccess)
+    return RTVLA_ERR_CUDA;
+  const bool rope = g.rope_theta > 0.f;
+  const size_t half = g.head_dim / 2, hi = ((size_t)g.table_width * g.page_size + 255) / 256;
+  const size_t parts = (size_t)pages_attend_parts(g.head_dim, group, c->sm_count) * group;
+  auto layout = [&](unsigned char *base) {
+    Carve take{c, base};
+    take(c->ctl, 1);
+    take(c->done, 1);
+    take(c->part_o, parts * g.head_dim);
+    take(c->part_ml, parts);
+    if (rope) {
+      take(c->rope_lo, 256 * half);
+      take(c->rope_hi, hi * half);
+    }
+    if (g.has_select) take(c->keys, (size_t)g.max_batch * g.n_kv_heads * g.table_width);
+    if (c->checked) take(c->d_guards, 16);  // one entry per buffer
+    return take.at;
+  };
+  const size_t bytes = layout(nullptr);
+  if (c->mem_cap && bytes > c->mem_cap) return RTVLA_ERR_OOM;
+  if (cudaMalloc(&c->arena, bytes) != cudaSuccess) {
+    c->arena = nullptr;
+    return RTVLA_ERR_OOM;
   }
-  const size_t parts = (size_t)pages_attend_parts(c->sm_count) * (g.n_q_heads / g.n_kv_heads);
-  c->part_o = p_alloc<float>(c, parts * g.head_dim);
-  c->part_ml = p_alloc<float2>(c, parts);
-  if (!c->part_o || !c->part_ml) return RTVLA_ERR_OOM;
-  if (g.has_select) {
-    c->keys = p_alloc<unsigned long long>(c, (size_t)g.max_batch * g.n_kv_heads * g.table_width);
-    if (!c->keys) return RTVLA_ERR_OOM;
-  }
-  DevCtl hc;
-  std::memset(&hc, 0, sizeof(hc));
-  if (cudaMemcpy(c->ctl, &hc, sizeof(hc), cudaMemcpyHostToDevice) != cudaSuccess) return RTVLA_ERR_CUDA;
+  layout(c->arena);
   if (c->checked) {
-    const size_t b = c->guards.size() * sizeof(GuardRegion);
-    if (cudaMalloc(&c->d_guards, b) != cudaSuccess ||
-        cudaMemcpy(c->d_guards, c->guards.data(), b, cudaMemcpyHostToDevice) != cudaSuccess)
+    for (const GuardRegion &r : c->guards)
+      if (cudaMemset(r.base, GUARD_FILL, GUARD_BYTES) != cudaSuccess ||
+          cudaMemset(r.base + GUARD_BYTES + r.bytes, GUARD_FILL, GUARD_BYTES) != cudaSuccess)
+        return RTVLA_ERR_CUDA;
+    if (cudaMemcpy(c->d_guards, c->guards.data(), c->guards.size() * sizeof(GuardRegion), cudaMemcpyHostToDevice) !=
+        cudaSuccess)
       return RTVLA_ERR_CUDA;
   }
+  if (cudaMemset(c->ctl, 0, sizeof(DevCtl)) != cudaSuccess || cudaMemset(c->done, 0, sizeof(int)) != cudaSuccess)
+    return RTVLA_ERR_CUDA;
+  if (rope && (launch_rope_table(c->rope_lo, 256, 1, g.head_dim, g.rope_theta, 0) != cudaSuccess ||
+               launch_rope_table(c->rope_hi, (int)hi, 256, g.head_dim, g.rope_theta, 0) != cudaSuccess))
+    return RTVLA_ERR_CUDA;
   return cudaDeviceSynchronize() == cudaSuccess ? RTVLA_OK : RTVLA_ERR_CUDA;
 }
 

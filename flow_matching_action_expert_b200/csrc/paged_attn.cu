@@ -14,17 +14,20 @@
 // pairs of tiles and one CTA per SM keep as much but leave an SM idle at the end of each request
 // (16 requests of 800 tokens: 13.8 us, with two CTAs 11.8; 64 of up to 32768: 178.7 and 181.3).
 //
-// Measured: 64 requests of up to 32768 tokens, 8 heads of 256 on one KV head (1.13 GB of K and V),
-// 181 us, 6.26 TB/s, 95% of the GPU's measured copy rate; 24 ragged requests, 32/8 heads of 128 in
-// f16 (351 MB) 65 us, 5.4 TB/s; one request of 131071 tokens (134 MB) 33 us, of which the reading
-// takes 21 and the start, the last tiles and the join the rest.  Short calls are latency: 8.3 us
-// for one request of 544 tokens.
+// The work is split evenly whatever the lengths (k_pages_attend): the 64-key chunks of all (request,
+// KV head) pairs, in order, are cut into one contiguous range per CTA.  A pair that lies inside one
+// range is finished there; of one that is cut each part goes to a workspace in fp32 and k_pages_join
+// adds the parts.  Both kernels find their place by summing the lengths themselves, so no plan has
+// to be made on the host and a captured graph stays valid when the lengths change.  (Adding the parts
+// in the attention kernel, by the CTA that finishes last, leaves one SM to do it: 16 requests of 800
+// tokens 14.3 us instead of 11.3, one of 131071 38.4 instead of 32.0.)  A few pairs of bounded length
+// go to k_pages_attend_cluster, which joins through shared memory.
 //
-// The work is split evenly whatever the lengths: the 64-key chunks of all (request, KV head)
-// pairs, in order, are cut into one contiguous range per CTA.  A pair that lies inside one range is
-// finished there; of one that is cut each part goes to a workspace in fp32 and k_pages_join adds
-// the parts.  Both kernels find their place by summing the lengths themselves, so no plan has to
-// be made on the host and a captured graph stays valid when the lengths change.
+// Measured: 64 requests of up to 32768 tokens, 8 heads of 256 on one KV head (1.13 GB of K and V),
+// 177 to 181 us, 6.3 TB/s, 96% of the GPU's measured copy rate; 24 ragged requests, 32/8 heads of 128
+// in f16 (351 MB) 65 us, 5.4 TB/s; one request of 131071 tokens (134 MB) 33 us, of which the reading
+// takes 21 and the start, the last tiles and the join the rest.  Short calls are latency: 7.9 us
+// for one request of 544 tokens, 9.8 for 16 of 800.
 //
 // Weights are split into two 16-bit halves, p = hi + lo, and multiplied twice: the products cost
 // nothing next to the loads, and the weights then count to 2^-16 instead of 2^-8.
@@ -44,6 +47,7 @@ constexpr int CHUNK = 64;  // keys per unit of work: one 16-key tile per warp
 constexpr int SETUP = 1;   // units that starting a pair and joining its warps count in the split
 constexpr int SLOTS = 3;   // ring of a warp: tiles of 16 rows, K and V in turn
 constexpr int MAX_CTAS = 1024;  // of one launch
+constexpr int CLUSTER = 8;      // CTAs that share a pair, when there are few pairs
 
 __device__ __forceinline__ void put(bf16 *p, float v) { *p = __float2bfloat16_rn(v); }
 __device__ __forceinline__ void put(__half *p, float v) { *p = __float2half_rn(v); }
@@ -121,6 +125,17 @@ struct Smem {
   static_assert(NT * 8 * OLD * 4 <= RING, "a warp's result fits its ring");
 };
 
+// the same variable of the cluster's CTA `rank`
+__device__ __forceinline__ const void *in_cta(const void *x, int rank) {
+  uint64_t at;
+  asm("mapa.u64 %0, %1, %2;" : "=l"(at) : "l"(reinterpret_cast<uint64_t>(x)), "r"(rank));
+  return reinterpret_cast<const void *>(at);
+}
+__device__ __forceinline__ void cluster_barrier() {
+  __syncwarp();
+  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+
 // CTAs that fit on an SM by shared memory (227 KB, 1 KB of it per CTA reserved)
 template <int D, int NT>
 constexpr int ctas_per_sm() {
@@ -128,19 +143,230 @@ constexpr int ctas_per_sm() {
   return fit < 4 ? fit : 4;
 }
 
+// Chunks [c0, c1) of request b and KV head h, of the n keys it attends to: every warp takes the tiles
+// `warp`, `warp` + 4, ...  Leaves each warp's result in its ring ([head][OLD] floats, unnormalised) and
+// its maximum (log2 units) and sum in ml_s, behind a barrier.
+template <typename T, int D, int NT>
+__device__ __forceinline__ void attend_chunks(const PagedAttnParams &p, uint8_t *smem, float2 (*ml_s)[NT * 8], int b,
+                                              int h, int len, int n, int c0, int c1, bool &bad) {
+  using S = Smem<D, NT>;
+  const PageGeom &g = p.g;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, gq = lane >> 2, t4 = lane & 3;
+  const int G = p.n_q_heads / g.n_kv_heads;
+  uint8_t *ring = smem + warp * S::RING;
+  const uint32_t ring_a = smem_u32(ring), q_a = smem_u32(smem + WARPS * S::RING);
+  const T *kp = static_cast<const T *>(p.k), *vp = static_cast<const T *>(p.v);
+  const int32_t *trow = p.table + (size_t)b * g.width;
+  const int32_t *sel = p.sel ? p.sel + ((size_t)b * g.n_kv_heads + h) * p.sel_width : nullptr;
+  const int tiles_end = min(c1 * 4, (n + 15) >> 4);
+
+  // row of the cache (all layers, pages and heads counted together) of key j, or ~0
+  auto row_of = [&](int j) -> uint32_t {
+    const int r = pg_key_row(trow, sel, j, n, len, g, &bad);
+    if (r < 0) return ~0u;
+    return (uint32_t)(((((size_t)p.layer * g.n_pages + (r >> g.shift)) * g.n_kv_heads + h) << g.shift) +
+                      (r & ((1 << g.shift) - 1)));
+  };
+  // requests the tile of K or V rows (lanes 0..15 hold them) into a slot, as one group
+  auto load = [&](const T *src, int slot, uint32_t rows) {
+    constexpr int CPR = D / 8, RPI = 32 / CPR;  // 16-byte chunks per row, rows per instruction
+    const int c = lane % CPR;
+#pragma unroll
+    for (int i = 0; i < 16 / RPI; ++i) {
+      const int r = i * RPI + lane / CPR;
+      const uint32_t at = __shfl_sync(0xffffffffu, rows, r);
+      const bool take = at != ~0u;
+      copy16(ring_a + slot * S::TILE + tile_at<D>(r, c), src + (take ? (size_t)at * D : 0) + c * 8, take);
+    }
+  };
+  auto rows_of = [&](int t) { return lane < 16 && t < tiles_end ? row_of(t * 16 + lane) : ~0u; };
+
+  // the ring holds K and V of this tile in slots `slot` and `slot` + 1
+  int tile = c0 * 4 + warp, slot = 0;
+  uint32_t row = rows_of(tile);
+  if (tile < tiles_end) load(kp, 0, row);
+  copy_commit();
+  if (tile < tiles_end) load(vp, 1, row);
+  copy_commit();
+  uint32_t live = __ballot_sync(0xffffffffu, row != ~0u);
+  row = rows_of(tile + WARPS);
+  // the group's query heads, zero rows past G
+  {
+    const T *q = static_cast<const T *>(p.q) + ((size_t)b * p.n_q_heads + h * G) * D;
+    for (int i = threadIdx.x; i < NT * 8 * (D / 8); i += WARPS * 32) {
+      const int r = i / (D / 8), c = i % (D / 8);
+      const uint4 v = r < G ? *reinterpret_cast<const uint4 *>(q + (size_t)r * D + c * 8) : make_uint4(0, 0, 0, 0);
+      *reinterpret_cast<uint4 *>(smem + WARPS * S::RING + tile_at<D>(r, c)) = v;
+    }
+  }
+  __syncthreads();
+
+  float o[D / 16][NT][4], m[NT][2], l[NT][2];
+#pragma unroll
+  for (int nt = 0; nt < NT; ++nt) {
+    m[nt][0] = m[nt][1] = -INFINITY;
+    l[nt][0] = l[nt][1] = 0.f;
+#pragma unroll
+    for (int i = 0; i < D / 16; ++i) o[i][nt][0] = o[i][nt][1] = o[i][nt][2] = o[i][nt][3] = 0.f;
+  }
+
+#pragma unroll 1
+  for (; tile < tiles_end; tile += WARPS) {
+    const int slot1 = slot == SLOTS - 1 ? 0 : slot + 1, slot2 = slot1 == SLOTS - 1 ? 0 : slot1 + 1;
+    const bool more = tile + WARPS < tiles_end;
+    const uint32_t ka = ring_a + slot * S::TILE, va = ring_a + slot1 * S::TILE;
+    copy_wait<1>();  // this tile's K
+    __syncwarp();    // and every lane is done with slot2, the last tile's V
+    if (more) load(kp, slot2, row);
+    copy_commit();
+
+    // S^T = K Q^T: rows (keys) gq and gq + 8, columns (heads) 2 t4 and 2 t4 + 1
+    float s[NT][2][4];
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) s[nt][0][e] = s[nt][1][e] = 0.f;
+#pragma unroll
+    for (int kk = 0; kk < D / 16; kk += 2) {
+      uint32_t a[2][4];
+#pragma unroll
+      for (int u = 0; u < 2; ++u)
+        ldsm_x4(a[u][0], a[u][1], a[u][2], a[u][3],
+                ka + tile_at<D>((lane & 7) + ((lane >> 3) & 1) * 8, 2 * (kk + u) + (lane >> 4)));
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt) {
+        uint32_t q0, q1, q2, q3;
+        ldsm_x4(q0, q1, q2, q3, q_a + tile_at<D>(nt * 8 + (lane & 7), 2 * kk + (lane >> 3)));
+        mma(s[nt][0], a[0], q0, q1, T());
+        mma(s[nt][1], a[1], q2, q3, T());
+      }
+    }
+    uint32_t hi[NT][2], lo[NT][2];
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+      float x[4];
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        x[e] = (live >> (gq + (e >> 1) * 8)) & 1 ? (s[nt][0][e] + s[nt][1][e]) * p.scale_log2 : -INFINITY;
+      float a[2];
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        float cm = fmaxf(x[e], x[e + 2]);
+#pragma unroll
+        for (int w = 4; w < 32; w <<= 1) cm = fmaxf(cm, __shfl_xor_sync(0xffffffffu, cm, w));
+        const float nm = fmaxf(m[nt][e], cm), ref = nm == -INFINITY ? 0.f : nm;
+        a[e] = exp2f(m[nt][e] - ref);
+        m[nt][e] = nm;
+        x[e] = exp2f(x[e] - ref);
+        x[e + 2] = exp2f(x[e + 2] - ref);
+        l[nt][e] = l[nt][e] * a[e] + (x[e] + x[e + 2]);
+      }
+      if (__any_sync(0xffffffffu, a[0] != 1.f || a[1] != 1.f)) {
+#pragma unroll
+        for (int i = 0; i < D / 16; ++i) {
+          o[i][nt][0] *= a[0];
+          o[i][nt][1] *= a[1];
+          o[i][nt][2] *= a[0];
+          o[i][nt][3] *= a[1];
+        }
+      }
+      split2(x[0], x[1], hi[nt][0], lo[nt][0], T());
+      split2(x[2], x[3], hi[nt][1], lo[nt][1], T());
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        hi[nt][e] = transpose8(hi[nt][e]);
+        lo[nt][e] = transpose8(lo[nt][e]);
+      }
+    }
+    copy_wait<1>();  // this tile's V
+    __syncwarp();    // and every lane is done with this tile's K
+    if (more) load(vp, slot, row);
+    copy_commit();
+    live = __ballot_sync(0xffffffffu, row != ~0u);
+    row = rows_of(tile + 2 * WARPS);
+    // O^T += V^T P^T: rows (components) 16 i + gq and + 8, columns (heads) 2 t4 and 2 t4 + 1
+#pragma unroll
+    for (int i = 0; i < D / 16; ++i) {
+      uint32_t a[4];
+      ldsm_x4_t(a[0], a[1], a[2], a[3],
+                va + tile_at<D>((lane & 7) + (lane >> 4) * 8, 2 * i + ((lane >> 3) & 1)));
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt) {
+        mma(o[i][nt], a, hi[nt][0], hi[nt][1], T());
+        mma(o[i][nt], a, lo[nt][0], lo[nt][1], T());
+      }
+    }
+    slot = slot2;
+  }
+  __syncwarp();
+
+  // ---- join the warps: each puts its result into its own ring
+  float *so = reinterpret_cast<float *>(ring);
+#pragma unroll
+  for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      float sum = l[nt][e];
+#pragma unroll
+      for (int w = 4; w < 32; w <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, w);
+      const int head = nt * 8 + 2 * t4 + e;
+      if (gq == 0) ml_s[warp][head] = make_float2(m[nt][e], sum);
+#pragma unroll
+      for (int i = 0; i < D / 16; ++i) {
+        so[head * S::OLD + 16 * i + gq] = o[i][nt][e];
+        so[head * S::OLD + 16 * i + gq + 8] = o[i][nt][e + 2];
+      }
+    }
+  __syncthreads();
+}
+
+// components d .. d + 3 of one head over the four warps' results; M and L: their maximum and sum
+template <int D, int NT>
+__device__ __forceinline__ float4 warps_sum(const uint8_t *smem, const float2 (*ml_s)[NT * 8], int head, int d, float &M,
+                                            float &L) {
+  using S = Smem<D, NT>;
+  M = -INFINITY;
+#pragma unroll
+  for (int w = 0; w < WARPS; ++w) M = fmaxf(M, ml_s[w][head].x);
+  const float ref = M == -INFINITY ? 0.f : M;
+  float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+  L = 0.f;
+#pragma unroll
+  for (int w = 0; w < WARPS; ++w) {
+    const float f = exp2f(ml_s[w][head].x - ref);
+    const float4 x =
+        *reinterpret_cast<const float4 *>(reinterpret_cast<const float *>(smem + w * S::RING) + head * S::OLD + d);
+    L += f * ml_s[w][head].y;
+    v.x += f * x.x;
+    v.y += f * x.y;
+    v.z += f * x.z;
+    v.w += f * x.w;
+  }
+  return v;
+}
+
+// four components of the output from their weighted sum and the sum of the weights
+template <typename T>
+__device__ __forceinline__ void put4(T *out, const float4 &v, float L) {
+  const float inv = L > 0.f ? 1.f / L : 0.f;
+  put(out, v.x * inv);
+  put(out + 1, v.y * inv);
+  put(out + 2, v.z * inv);
+  put(out + 3, v.w * inv);
+}
+
 }  // namespace
 
 // NT: query heads in tiles of 8 (1: G <= 8, 2: G <= 16)
 template <typename T, int D, int NT>
 __global__ void __launch_bounds__(WARPS * 32, ctas_per_sm<D, NT>()) k_pages_attend(PagedAttnParams p) {
-  using S = Smem<D, NT>;
   extern __shared__ __align__(128) uint8_t smem[];
   __shared__ long long warp_sum_s[WARPS];
   __shared__ long long first_at;
   __shared__ int first_b;
   __shared__ float2 ml_s[WARPS][NT * 8];
   const PageGeom g = p.g;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, gq = lane >> 2, t4 = lane & 3;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int G = p.n_q_heads / g.n_kv_heads, B = p.batch;
   // Launched while the kernel before it may still run (rtvla_pages_write and _select let it), so
   // nothing is read before this; the join is launched likewise.
@@ -194,213 +420,28 @@ __global__ void __launch_bounds__(WARPS * 32, ctas_per_sm<D, NT>()) k_pages_atte
   int h = min((int)quotient(first_at, n_units), g.n_kv_heads - 1), u0 = (int)(first_at - (long long)h * n_units);
   long long at = start;  // unit of the whole work
 
-  uint8_t *ring = smem + warp * S::RING;
-  const uint32_t ring_a = smem_u32(ring), q_a = smem_u32(smem + WARPS * S::RING);
-  const T *kp = static_cast<const T *>(p.k), *vp = static_cast<const T *>(p.v);
-
   while (true) {
     // ---- one segment: chunks [c0, c1) of (b, h)
     const int u1 = (int)min((long long)n_units, u0 + (end - at));
     const int c0 = max(u0 - SETUP, 0), c1 = u1 - SETUP, n_chunks = n_units - SETUP;
     if (c1 > c0) {
-    const int len = pg_len(p.lens[b], g, &bad);
-    const int n = pg_list_len(len, p.sel_width, p.sel != nullptr, g);
-    const int32_t *trow = p.table + (size_t)b * g.width;
-    const int32_t *sel = p.sel ? p.sel + ((size_t)b * g.n_kv_heads + h) * p.sel_width : nullptr;
-    const int tiles_end = min(c1 * 4, (n + 15) >> 4);
-
-    // row of the cache (all layers, pages and heads counted together) of key j, or ~0
-    auto row_of = [&](int j) -> uint32_t {
-      const int r = pg_key_row(trow, sel, j, n, len, g, &bad);
-      if (r < 0) return ~0u;
-      return (uint32_t)(((((size_t)p.layer * g.n_pages + (r >> g.shift)) * g.n_kv_heads + h) << g.shift) +
-                        (r & ((1 << g.shift) - 1)));
-    };
-    // requests the tile of K or V rows (lanes 0..15 hold them) into a slot, as one group
-    auto load = [&](const T *src, int slot, uint32_t rows) {
-      constexpr int CPR = D / 8, RPI = 32 / CPR;  // 16-byte chunks per row, rows per instruction
-      const int c = lane % CPR;
-#pragma unroll
-      for (int i = 0; i < 16 / RPI; ++i) {
-        const int r = i * RPI + lane / CPR;
-        const uint32_t at = __shfl_sync(0xffffffffu, rows, r);
-        const bool take = at != ~0u;
-        copy16(ring_a + slot * S::TILE + tile_at<D>(r, c), src + (take ? (size_t)at * D : 0) + c * 8, take);
-      }
-    };
-    auto rows_of = [&](int t) { return lane < 16 && t < tiles_end ? row_of(t * 16 + lane) : ~0u; };
-
-    // the ring holds K and V of this tile in slots `slot` and `slot` + 1
-    int tile = c0 * 4 + warp, slot = 0;
-    uint32_t row = rows_of(tile);
-    if (tile < tiles_end) load(kp, 0, row);
-    copy_commit();
-    if (tile < tiles_end) load(vp, 1, row);
-    copy_commit();
-    uint32_t live = __ballot_sync(0xffffffffu, row != ~0u);
-    row = rows_of(tile + WARPS);
-    // the group's query heads, zero rows past G
-    {
-      const T *q = static_cast<const T *>(p.q) + ((size_t)b * p.n_q_heads + h * G) * D;
-      for (int i = threadIdx.x; i < NT * 8 * (D / 8); i += WARPS * 32) {
-        const int r = i / (D / 8), c = i % (D / 8);
-        const uint4 v = r < G ? *reinterpret_cast<const uint4 *>(q + (size_t)r * D + c * 8) : make_uint4(0, 0, 0, 0);
-        *reinterpret_cast<uint4 *>(smem + WARPS * S::RING + tile_at<D>(r, c)) = v;
-      }
-    }
-    __syncthreads();
-
-    float o[D / 16][NT][4], m[NT][2], l[NT][2];
-#pragma unroll
-    for (int nt = 0; nt < NT; ++nt) {
-      m[nt][0] = m[nt][1] = -INFINITY;
-      l[nt][0] = l[nt][1] = 0.f;
-#pragma unroll
-      for (int i = 0; i < D / 16; ++i) o[i][nt][0] = o[i][nt][1] = o[i][nt][2] = o[i][nt][3] = 0.f;
-    }
-
-#pragma unroll 1
-    for (; tile < tiles_end; tile += WARPS) {
-      const int slot1 = slot == SLOTS - 1 ? 0 : slot + 1, slot2 = slot1 == SLOTS - 1 ? 0 : slot1 + 1;
-      const bool more = tile + WARPS < tiles_end;
-      const uint32_t ka = ring_a + slot * S::TILE, va = ring_a + slot1 * S::TILE;
-      copy_wait<1>();  // this tile's K
-      __syncwarp();    // and every lane is done with slot2, the last tile's V
-      if (more) load(kp, slot2, row);
-      copy_commit();
-
-      // S^T = K Q^T: rows (keys) gq and gq + 8, columns (heads) 2 t4 and 2 t4 + 1
-      float s[NT][2][4];
-#pragma unroll
-      for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) s[nt][0][e] = s[nt][1][e] = 0.f;
-#pragma unroll
-      for (int kk = 0; kk < D / 16; kk += 2) {
-        uint32_t a[2][4];
-#pragma unroll
-        for (int u = 0; u < 2; ++u)
-          ldsm_x4(a[u][0], a[u][1], a[u][2], a[u][3],
-                  ka + tile_at<D>((lane & 7) + ((lane >> 3) & 1) * 8, 2 * (kk + u) + (lane >> 4)));
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt) {
-          uint32_t q0, q1, q2, q3;
-          ldsm_x4(q0, q1, q2, q3, q_a + tile_at<D>(nt * 8 + (lane & 7), 2 * kk + (lane >> 3)));
-          mma(s[nt][0], a[0], q0, q1, T());
-          mma(s[nt][1], a[1], q2, q3, T());
+      const int len = pg_len(p.lens[b], g, &bad);
+      const int n = pg_list_len(len, p.sel_width, p.sel != nullptr, g);
+      attend_chunks<T, D, NT>(p, smem, ml_s, b, h, len, n, c0, c1, bad);
+      const bool whole = c0 == 0 && c1 == n_chunks;
+      // a CTA's parts: of a pair that began before it, and of one that goes on after it
+      const size_t part = (size_t)blockIdx.x * 2 + (c0 == 0 ? 1 : 0);
+      for (int i = threadIdx.x; i < G * (D / 4); i += WARPS * 32) {
+        const int head = i / (D / 4), d = (i % (D / 4)) * 4;
+        float M, L;
+        const float4 v = warps_sum<D, NT>(smem, ml_s, head, d, M, L);
+        if (whole) {
+          put4(static_cast<T *>(p.out) + ((size_t)b * p.n_q_heads + h * G + head) * D + d, v, L);
+        } else {
+          *reinterpret_cast<float4 *>(p.part_o + (part * G + head) * D + d) = v;
+          if (d == 0) p.part_ml[part * G + head] = make_float2(M, L);
         }
       }
-      uint32_t hi[NT][2], lo[NT][2];
-#pragma unroll
-      for (int nt = 0; nt < NT; ++nt) {
-        float x[4];
-#pragma unroll
-        for (int e = 0; e < 4; ++e)
-          x[e] = (live >> (gq + (e >> 1) * 8)) & 1 ? (s[nt][0][e] + s[nt][1][e]) * p.scale_log2 : -INFINITY;
-        float a[2];
-#pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          float cm = fmaxf(x[e], x[e + 2]);
-#pragma unroll
-          for (int w = 4; w < 32; w <<= 1) cm = fmaxf(cm, __shfl_xor_sync(0xffffffffu, cm, w));
-          const float nm = fmaxf(m[nt][e], cm), ref = nm == -INFINITY ? 0.f : nm;
-          a[e] = exp2f(m[nt][e] - ref);
-          m[nt][e] = nm;
-          x[e] = exp2f(x[e] - ref);
-          x[e + 2] = exp2f(x[e + 2] - ref);
-          l[nt][e] = l[nt][e] * a[e] + (x[e] + x[e + 2]);
-        }
-        if (__any_sync(0xffffffffu, a[0] != 1.f || a[1] != 1.f)) {
-#pragma unroll
-          for (int i = 0; i < D / 16; ++i) {
-            o[i][nt][0] *= a[0];
-            o[i][nt][1] *= a[1];
-            o[i][nt][2] *= a[0];
-            o[i][nt][3] *= a[1];
-          }
-        }
-        split2(x[0], x[1], hi[nt][0], lo[nt][0], T());
-        split2(x[2], x[3], hi[nt][1], lo[nt][1], T());
-#pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          hi[nt][e] = transpose8(hi[nt][e]);
-          lo[nt][e] = transpose8(lo[nt][e]);
-        }
-      }
-      copy_wait<1>();  // this tile's V
-      __syncwarp();    // and every lane is done with this tile's K
-      if (more) load(vp, slot, row);
-      copy_commit();
-      live = __ballot_sync(0xffffffffu, row != ~0u);
-      row = rows_of(tile + 2 * WARPS);
-      // O^T += V^T P^T: rows (components) 16 i + gq and + 8, columns (heads) 2 t4 and 2 t4 + 1
-#pragma unroll
-      for (int i = 0; i < D / 16; ++i) {
-        uint32_t a[4];
-        ldsm_x4_t(a[0], a[1], a[2], a[3],
-                  va + tile_at<D>((lane & 7) + (lane >> 4) * 8, 2 * i + ((lane >> 3) & 1)));
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt) {
-          mma(o[i][nt], a, hi[nt][0], hi[nt][1], T());
-          mma(o[i][nt], a, lo[nt][0], lo[nt][1], T());
-        }
-      }
-      slot = slot2;
-    }
-    __syncwarp();
-
-    // ---- join the warps: each puts its result into its own ring
-    float *so = reinterpret_cast<float *>(ring);
-#pragma unroll
-    for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        float sum = l[nt][e];
-#pragma unroll
-        for (int w = 4; w < 32; w <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, w);
-        const int head = nt * 8 + 2 * t4 + e;
-        if (gq == 0) ml_s[warp][head] = make_float2(m[nt][e], sum);
-#pragma unroll
-        for (int i = 0; i < D / 16; ++i) {
-          so[head * S::OLD + 16 * i + gq] = o[i][nt][e];
-          so[head * S::OLD + 16 * i + gq + 8] = o[i][nt][e + 2];
-        }
-      }
-    __syncthreads();
-    const bool whole = c0 == 0 && c1 == n_chunks;
-    // a CTA's parts: of a pair that began before it, and of one that goes on after it
-    const size_t part = (size_t)blockIdx.x * 2 + (c0 == 0 ? 1 : 0);
-    for (int i = threadIdx.x; i < G * (D / 4); i += WARPS * 32) {
-      const int head = i / (D / 4), d = (i % (D / 4)) * 4;
-      float M = -INFINITY, L = 0.f;
-#pragma unroll
-      for (int w = 0; w < WARPS; ++w) M = fmaxf(M, ml_s[w][head].x);
-      const float ref = M == -INFINITY ? 0.f : M;
-      float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll
-      for (int w = 0; w < WARPS; ++w) {
-        const float f = exp2f(ml_s[w][head].x - ref);
-        const float4 x = *reinterpret_cast<const float4 *>(reinterpret_cast<float *>(smem + w * S::RING) +
-                                                           head * S::OLD + d);
-        L += f * ml_s[w][head].y;
-        v.x += f * x.x;
-        v.y += f * x.y;
-        v.z += f * x.z;
-        v.w += f * x.w;
-      }
-      if (whole) {
-        const float inv = L > 0.f ? 1.f / L : 0.f;
-        T *out = static_cast<T *>(p.out) + ((size_t)b * p.n_q_heads + h * G + head) * D + d;
-        put(out, v.x * inv);
-        put(out + 1, v.y * inv);
-        put(out + 2, v.z * inv);
-        put(out + 3, v.w * inv);
-      } else {
-        *reinterpret_cast<float4 *>(p.part_o + (part * G + head) * D + d) = v;
-        if (d == 0) p.part_ml[part * G + head] = make_float2(M, L);
-      }
-    }
-
     }
     at += u1 - u0;
     if (at >= end) break;
@@ -422,6 +463,66 @@ __global__ void __launch_bounds__(WARPS * 32, ctas_per_sm<D, NT>()) k_pages_atte
     }
   }
   if (bad) set_error(p.ctl, DEVERR_BOUNDS, PG_AT_ATTEND);
+}
+
+// The same for few pairs of bounded length: a cluster per (request, KV head), its CTAs share the
+// chunks evenly and add their results through each other's shared memory, so that there is neither
+// a workspace nor a second kernel.
+template <typename T, int D, int NT>
+__global__ void __cluster_dims__(CLUSTER, 1, 1) __launch_bounds__(WARPS * 32, ctas_per_sm<D, NT>())
+    k_pages_attend_cluster(PagedAttnParams p) {
+  using S = Smem<D, NT>;
+  extern __shared__ __align__(128) uint8_t smem[];
+  __shared__ float2 ml_s[WARPS][NT * 8], sum_s[NT * 8];
+  const PageGeom g = p.g;
+  const int rank = blockIdx.x, h = blockIdx.y, b = blockIdx.z, G = p.n_q_heads / g.n_kv_heads;
+  asm volatile("griddepcontrol.wait;" ::: "memory");  // as k_pages_attend
+  bool bad = false;
+  const int len = pg_len(p.lens[b], g, &bad);
+  const int n = pg_list_len(len, p.sel_width, p.sel != nullptr, g), chunks = (n + CHUNK - 1) / CHUNK;
+  const int c0 = chunks * rank / CLUSTER, c1 = chunks * (rank + 1) / CLUSTER;
+  if (c1 > c0) {
+    attend_chunks<T, D, NT>(p, smem, ml_s, b, h, len, n, c0, c1, bad);
+    // the warps' sum takes the place of warp 0's result: a thread reads and writes its own components
+    for (int i = threadIdx.x; i < G * (D / 4); i += WARPS * 32) {
+      const int head = i / (D / 4), d = (i % (D / 4)) * 4;
+      float M, L;
+      const float4 v = warps_sum<D, NT>(smem, ml_s, head, d, M, L);
+      *reinterpret_cast<float4 *>(reinterpret_cast<float *>(smem) + head * S::OLD + d) = v;
+      if (d == 0) sum_s[head] = make_float2(M, L);
+    }
+  } else if (threadIdx.x < NT * 8) {
+    sum_s[threadIdx.x] = make_float2(-INFINITY, 0.f);
+  }
+  if (bad) set_error(p.ctl, DEVERR_BOUNDS, PG_AT_ATTEND);
+  cluster_barrier();
+  // each CTA adds a share of the components over all of them
+  for (int i = rank * WARPS * 32 + threadIdx.x; i < G * (D / 4); i += CLUSTER * WARPS * 32) {
+    const int head = i / (D / 4), d = (i % (D / 4)) * 4;
+    float2 ml[CLUSTER];
+    float4 x[CLUSTER];
+    float M = -INFINITY, L = 0.f;
+#pragma unroll
+    for (int r = 0; r < CLUSTER; ++r) {
+      ml[r] = *static_cast<const float2 *>(in_cta(&sum_s[head], r));
+      x[r] = *static_cast<const float4 *>(in_cta(reinterpret_cast<float *>(smem) + head * S::OLD + d, r));
+      M = fmaxf(M, ml[r].x);
+    }
+    const float ref = M == -INFINITY ? 0.f : M;
+    float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+    for (int r = 0; r < CLUSTER; ++r) {
+      if (ml[r].x == -INFINITY && ml[r].y == 0.f) continue;  // no keys: its shared memory holds no result
+      const float f = exp2f(ml[r].x - ref);
+      L += f * ml[r].y;
+      v.x += f * x[r].x;
+      v.y += f * x[r].y;
+      v.z += f * x[r].z;
+      v.w += f * x[r].w;
+    }
+    put4(static_cast<T *>(p.out) + ((size_t)b * p.n_q_heads + h * G + head) * D + d, v, L);
+  }
+  cluster_barrier();  // no CTA leaves while others read its shared memory
 }
 
 // Adds the parts of one (request, query head) that was cut across CTAs of k_pages_attend, and
@@ -541,32 +642,39 @@ __global__ void __launch_bounds__(JOIN_THREADS) k_pages_join(PagedAttnParams p, 
     v.z += x.z;
     v.w += x.w;
   }
-  const float inv = L > 0.f ? 1.f / L : 0.f;
-  put(out + col * 4, v.x * inv);
-  put(out + col * 4 + 1, v.y * inv);
-  put(out + col * 4 + 2, v.z * inv);
-  put(out + col * 4 + 3, v.w * inv);
+  put4(out + col * 4, v, L);
 }
 
 namespace {
 
 template <typename T, int D, int NT>
 cudaError_t attend(const PagedAttnParams &p, int sm_count, cudaStream_t st) {
-  // one wave of CTAs, but no more than there can be units
-  const long long keys = (long long)(p.sel && p.sel_width < p.g.width ? p.sel_width : p.g.width) << p.g.shift;
-  const long long most = (long long)p.batch * p.g.n_kv_heads * ((keys + CHUNK - 1) / CHUNK + SETUP);
-  const long long wave = std::min(sm_count * ctas_per_sm<D, NT>(), MAX_CTAS);
-  const int ctas = (int)(most < wave ? most : wave);
   cudaLaunchAttribute attr;
   attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr.val.programmaticStreamSerializationAllowed = 1;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(ctas);
   cfg.blockDim = dim3(WARPS * 32);
   cfg.dynamicSmemBytes = Smem<D, NT>::TOTAL;
   cfg.stream = st;
   cfg.attrs = &attr;
   cfg.numAttrs = 1;
+  const long long keys = (long long)(p.sel && p.sel_width < p.g.width ? p.sel_width : p.g.width) << p.g.shift;
+  const long long wave = std::min(sm_count * ctas_per_sm<D, NT>(), MAX_CTAS);
+  const long long pairs = (long long)p.batch * p.g.n_kv_heads, chunks = (keys + CHUNK - 1) / CHUNK;
+  // Clusters save the parts and the second launch, about 2.5 us, but give a CTA up to chunks / CLUSTER
+  // chunks where an even split over the whole wave gives fewer; one more costs 1.4 us at d = 256 and
+  // 0.8 below.  One request of 1000 tokens: 7.5 us (split 8.1), of 2000: 10.4 (8.7) at d = 256, 8.0
+  // (8.3) at d = 128; 16 requests of 1000: 10.1 (12.7).  Past half a wave clusters no longer fit at once
+  // (37 requests of 1000: 20.3, split 17.6).
+  const long long most_c = (chunks + CLUSTER - 1) / CLUSTER, most_s = (pairs * (chunks + SETUP) + wave - 1) / wave;
+  if (pairs * CLUSTER * 2 <= wave && most_c - most_s <= (D == 256 ? 1 : 3)) {
+    cfg.gridDim = dim3(CLUSTER, p.g.n_kv_heads, p.batch);
+    return cudaLaunchKernelEx(&cfg, k_pages_attend_cluster<T, D, NT>, p);
+  }
+  // otherwise one wave of CTAs, but no more than there can be units
+  const long long most = pairs * (chunks + SETUP);
+  const int ctas = (int)(most < wave ? most : wave);
+  cfg.gridDim = dim3(ctas);
   const cudaError_t e = cudaLaunchKernelEx(&cfg, k_pages_attend<T, D, NT>, p);
   if (e != cudaSuccess) return e;
   // Few (request, head) pairs have many parts each and take 512 threads; many pairs have few parts,
@@ -591,12 +699,18 @@ cudaError_t attend(const PagedAttnParams &p, int sm_count, cudaStream_t st) {
   return p.g.head_dim == 128 ? attend<T, 128>(p, sm_count, st) : attend<T, 256>(p, sm_count, st);
 }
 
+template <typename T, int D, int NT>
+cudaError_t allow_smem() {
+  const cudaError_t e =
+      cudaFuncSetAttribute(k_pages_attend<T, D, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize, Smem<D, NT>::TOTAL);
+  return e != cudaSuccess ? e
+                          : cudaFuncSetAttribute(k_pages_attend_cluster<T, D, NT>,
+                                                 cudaFuncAttributeMaxDynamicSharedMemorySize, Smem<D, NT>::TOTAL);
+}
+
 template <typename T, int D>
 cudaError_t allow_smem(int group) {
-  return group <= 8 ? cudaFuncSetAttribute(k_pages_attend<T, D, 1>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                           Smem<D, 1>::TOTAL)
-                    : cudaFuncSetAttribute(k_pages_attend<T, D, 2>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                           Smem<D, 2>::TOTAL);
+  return group <= 8 ? allow_smem<T, D, 1>() : allow_smem<T, D, 2>();
 }
 
 template <typename T>

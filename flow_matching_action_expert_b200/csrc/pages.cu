@@ -607,6 +607,7 @@ __global__ void __cluster_dims__(SC, 1, 1) __launch_bounds__(ST, 2) k_pages_sele
     if (lane == 0) static_cast<uint32_t *>(in_first(big_mean))[rank * (ST / 32) + warp] = most;
     if (bad) set_error(p.ctl, DEVERR_BOUNDS, PG_AT_SELECT);
   }
+  __syncwarp();
   asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
   if (rank != 0) return;
 

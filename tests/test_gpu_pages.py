@@ -101,8 +101,9 @@ EDGE = [0, 1, 2, 15, 16, 17, 31, 63, 64, 65, 127, 128, 129, 200, 0, 333]
 @pytest.mark.parametrize("dtype", ["bf16", "f16"])
 @pytest.mark.parametrize("hq, hkv, d, page", [(8, 1, 256, 16), (1, 1, 256, 64), (16, 1, 256, 1), (8, 8, 128, 32),
                                               (14, 2, 128, 8), (9, 3, 64, 256), (32, 2, 64, 2), (7, 1, 64, 1024)])
-def test_attend_over_edge_lengths(dtype, hq, hkv, d, page):
-    c = Cache(EDGE, dtype, hq, hkv, d, page, layers=2)
+@pytest.mark.parametrize("room", [None, 8192])  # tokens a table row has room for: it decides how work is split
+def test_attend_over_edge_lengths(dtype, hq, hkv, d, page, room):
+    c = Cache(EDGE, dtype, hq, hkv, d, page, layers=2, width=room and OP.pages_for(room, page))
     for layer in (1, 0):
         c.check_attend(c.attend(layer), layer)
 

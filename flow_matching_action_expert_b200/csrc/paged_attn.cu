@@ -322,8 +322,8 @@ __device__ __forceinline__ void attend_chunks(const PagedAttnParams &p, uint8_t 
 
 // components d .. d + 3 of one head over the four warps' results; M and L: their maximum and sum
 template <int D, int NT>
-__device__ __forceinline__ float4 warps_sum(const uint8_t *smem, const float2 (*ml_s)[NT * 8], int head, int d, float &M,
-                                            float &L) {
+__device__ __forceinline__ float4 warps_sum(const uint8_t *smem, const float2 (*ml_s)[NT * 8], int head, int d,
+                                            float &M, float &L) {
   using S = Smem<D, NT>;
   M = -INFINITY;
 #pragma unroll
@@ -568,7 +568,8 @@ __global__ void __launch_bounds__(JOIN_THREADS) k_pages_join(PagedAttnParams p, 
   const long long x0 = before * g.n_kv_heads + n * h, x1 = x0 + n;
   const long long ctas = max(min(total, (long long)grid), 1ll);
   // unit x belongs to the CTA c with total c / ctas <= x < total (c + 1) / ctas
-  const int from = n ? (int)quotient((x0 + SETUP + 1) * ctas - 1, total) : 0, to = n ? (int)quotient(x1 * ctas - 1, total) : 0;
+  const int from = n ? (int)quotient((x0 + SETUP + 1) * ctas - 1, total) : 0;
+  const int to = n ? (int)quotient(x1 * ctas - 1, total) : 0;
   asm volatile("griddepcontrol.wait;" ::: "memory");
   if (n == 0) {
     for (int i = threadIdx.x; i < W; i += JOIN_THREADS) put(out + i, 0.f);
@@ -722,10 +723,10 @@ cudaError_t allow_smem(int head_dim, int group) {
 }  // namespace
 
 int pages_attend_parts(int head_dim, int group, int sm_count) {
-  int ctas;
-  if (group <= 8) ctas = head_dim == 64 ? ctas_per_sm<64, 1>() : head_dim == 128 ? ctas_per_sm<128, 1>() : ctas_per_sm<256, 1>();
-  else ctas = head_dim == 64 ? ctas_per_sm<64, 2>() : head_dim == 128 ? ctas_per_sm<128, 2>() : ctas_per_sm<256, 2>();
-  return 2 * std::min(ctas * sm_count, MAX_CTAS);
+  const int at = head_dim == 64 ? 0 : head_dim == 128 ? 1 : 2;
+  const int one[] = {ctas_per_sm<64, 1>(), ctas_per_sm<128, 1>(), ctas_per_sm<256, 1>()};
+  const int two[] = {ctas_per_sm<64, 2>(), ctas_per_sm<128, 2>(), ctas_per_sm<256, 2>()};
+  return 2 * std::min((group <= 8 ? one : two)[at] * sm_count, MAX_CTAS);
 }
 
 cudaError_t pages_attend_init_attributes(int dtype, int head_dim, int group) {

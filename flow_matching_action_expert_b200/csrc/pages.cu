@@ -217,8 +217,8 @@ size_t plan_smem(int batch) { return (size_t)(5 * batch + 3) * sizeof(int); }
 namespace {
 
 constexpr int WT = 256;       // threads of a write CTA
+constexpr int MEAN_CTAS = 2;  // per SM, that look for filled pages
 constexpr int HEADS = 4;      // heads a thread moves: their loads are in flight together
-constexpr int MEAN_ROWS = 16; // rows a CTA searches for pages they fill
 
 // eight consecutive values as they lie in memory, and in fp32
 template <typename S>
@@ -278,15 +278,15 @@ __device__ __forceinline__ void rotate8(float (&x1)[8], float (&x2)[8], const fl
 
 // Moves bytes: a row is read once and written once, with two table rows of 8 bytes per pair that
 // its heads share through L1.  A thread takes eight pairs (16 bytes of each half) of HEADS heads.
-// Measured: 4348 rows of 10 heads of 256 (44 MB) 13.0 us, 3.4 TB/s: two waves of CTAs, each as long
-// as its chain of loads (slot, then table row).  Two heads per thread take 13.6 us; 64 registers
-// instead of 80 spill (14.9); CTAs of 128 threads with five heads take 11.8 but add 0.5 us to a
-// decode step of 16 rows, now 4.9.
-// The first CTAs look for rows that fill their page.  The mean of such a page needs the rows of this
-// call that other CTAs write, so it is computed from their sources again; the page's earlier keys
-// come from the pool.
+// Measured: 4348 rows of 10 heads of 256 (44 MB) 13 us, 3.4 TB/s: two waves of CTAs, each as long as
+// its chain of loads (slot, then table row); 9465 rows 23.6 us, 4.1 TB/s.  Two heads per thread take
+// 13.6 us; 64 registers instead of 80 spill (14.9).  A decode step of 16 rows: 4.9 us.
+// The first CTAs look for rows that fill their page, one KV head each, several small pages at a time
+// (16 rows of 32 + 16 heads of 128: 3.8 us; with all heads and pages in turn 13.3).  The mean of such a page needs
+// the rows of this call that other CTAs write, so it is computed from their sources again; the page's
+// earlier keys come from the pool.
 template <typename T, typename S>
-__global__ void __launch_bounds__(WT) k_pages_write(WriteParams p, int mean_ctas) {
+__global__ void __launch_bounds__(WT) k_pages_write(WriteParams p, int mean_ctas, int mean_rows) {
   const PageGeom g = p.g;
   const int d = g.head_dim, half = d / 2, blocks = d / 16;  // blocks of eight pairs
   const int hq = p.n_q_heads, hkv = g.n_kv_heads, heads = hq + 2 * hkv, cap = g.width << g.shift;
@@ -334,65 +334,73 @@ __global__ void __launch_bounds__(WT) k_pages_write(WriteParams p, int mean_ctas
   }
   // ---- page means
   __shared__ float sums[WT * 16];  // [WT / blocks][d]
-  __shared__ int run;
+  __shared__ int slot_s[WT / 4];
   const int ps = 1 << g.shift, i8 = threadIdx.x % blocks, lane_r = threadIdx.x / blocks, n_lanes = WT / blocks;
-  const int r0 = (int)blockIdx.x * MEAN_ROWS;
-  // every warp looks at all the rows of this CTA, a row per lane
-  const int lane = threadIdx.x & 31, my_r = r0 + lane;
-  int my_slot = -1;
-  if (lane < MEAN_ROWS && my_r < p.n_rows) {
-    bool bad = false;
-    my_slot = pg_slot(p.slots[my_r], g, &bad);
-    const int at = p.positions[my_r];
-    if (at < 0 || at >= cap || (my_slot & (ps - 1)) != ps - 1) my_slot = -1;
-  }
-  for (unsigned fills = __ballot_sync(0xffffffffu, my_slot >= 0); fills; fills &= fills - 1) {
-    const int i = __ffs(fills) - 1, r = r0 + i, slot = __shfl_sync(0xffffffffu, my_slot, i);
-    // rows r, r - 1, ... fill the page downwards as far as their slots run on
-    const int most = min(ps, r + 1);
-    __syncthreads();
-    if (threadIdx.x == 0) run = most;
-    __syncthreads();
-    for (int i = threadIdx.x; i < most; i += WT)
-      if (p.slots[r - i] != slot - i) atomicMin(&run, i);
-    __syncthreads();
-    const int from = ps - run;
-    for (int h = 0; h < hkv; ++h) {
+  // `team` row lanes add the keys of a page, `teams` pages at a time
+  const int team = min(ps, n_lanes), teams = n_lanes / team, my_team = lane_r / team;
+  // this CTA's KV head, and its rows; every warp looks at 32 of them at a time, one per lane
+  const int h = (int)blockIdx.x % hkv, r0 = (int)blockIdx.x / hkv * mean_rows, r1 = min(p.n_rows, r0 + mean_rows);
+  const int lane = threadIdx.x & 31;
+  for (int g0 = r0; g0 < r1; g0 += 32) {
+    int my_slot = -1;  // of a row that fills its page
+    if (g0 + lane < r1) {
+      bool bad = false;
+      my_slot = pg_slot(p.slots[g0 + lane], g, &bad);
+      const int at = p.positions[g0 + lane];
+      if (at < 0 || at >= cap || (my_slot & (ps - 1)) != ps - 1) my_slot = -1;
+    }
+    unsigned fills = __ballot_sync(0xffffffffu, my_slot >= 0);
+    while (fills) {
+      unsigned mine = fills;  // this team's page is the my_team-th
+      for (int t = 0; t < teams && fills; ++t) {
+        if (t < my_team) mine &= mine - 1;
+        fills &= fills - 1;
+      }
+      const int i = mine ? __ffs(mine) - 1 : 0, r = g0 + i;
+      int slot = __shfl_sync(0xffffffffu, my_slot, i);
+      if (!mine) slot = -1;
       float a1[8] = {0, 0, 0, 0, 0, 0, 0, 0}, a2[8] = {0, 0, 0, 0, 0, 0, 0, 0};
+      if (slot >= 0) {
 #pragma unroll 2
-      for (int o = lane_r; o < ps; o += n_lanes) {
-        float x1[8], x2[8];
-        if (o < from) {
-          const T *x = k + pg_elem(p.layer, slot - (ps - 1) + o, h, g) + i8 * 8;
-          load8(x1, x);
-          load8(x2, x + half);
-        } else {
-          const int row = r - (ps - 1 - o), pos = min(max(p.positions[row], 0), cap - 1);
-          const S *x = src + row * ld + (size_t)(hq + h) * d + i8 * 8;
-          load8(x1, x);
-          load8(x2, x + half);
-          if (p.rope_lo) {
-            float c[8], s[8];
-            rope8(c, s, p, pos, i8, half);
-            rotate8(x1, x2, c, s);
+        for (int o = lane_r % team; o < ps; o += team) {
+          float x1[8], x2[8];
+          // the key `back` tokens before: of this call's row as far before, if that has its slot
+          const int back = ps - 1 - o, row = r - back;
+          if (row >= 0 && p.slots[row] == slot - back) {
+            const int pos = min(max(p.positions[row], 0), cap - 1);
+            const S *x = src + row * ld + (size_t)(hq + h) * d + i8 * 8;
+            load8(x1, x);
+            load8(x2, x + half);
+            if (p.rope_lo) {
+              float c[8], s[8];
+              rope8(c, s, p, pos, i8, half);
+              rotate8(x1, x2, c, s);
+            }
+          } else {
+            const T *x = k + pg_elem(p.layer, slot - back, h, g) + i8 * 8;
+            load8(x1, x);
+            load8(x2, x + half);
+          }
+#pragma unroll
+          for (int u = 0; u < 8; ++u) {  // keys as stored
+            a1[u] += to_f(from_f<T>(x1[u]));
+            a2[u] += to_f(from_f<T>(x2[u]));
           }
         }
-#pragma unroll
-        for (int u = 0; u < 8; ++u) {  // keys as stored
-          a1[u] += to_f(from_f<T>(x1[u]));
-          a2[u] += to_f(from_f<T>(x2[u]));
-        }
       }
+      if (lane_r % team == 0 && i8 == 0) slot_s[my_team] = slot;
 #pragma unroll
       for (int u = 0; u < 8; ++u) {
         sums[lane_r * d + i8 * 8 + u] = a1[u];
         sums[lane_r * d + half + i8 * 8 + u] = a2[u];
       }
       __syncthreads();
-      for (int i = threadIdx.x; i < d; i += WT) {
+      for (int at = threadIdx.x; at < teams * d; at += WT) {
+        const int t = at / d, x = at % d;
+        if (slot_s[t] < 0) continue;
         float sum = 0.f;
-        for (int l = 0; l < min(n_lanes, ps); ++l) sum += sums[l * d + i];
-        static_cast<T *>(p.k_mean)[pg_mean_elem(p.layer, slot >> g.shift, h, g) + i] = from_f<T>(sum / ps);
+        for (int l = 0; l < team; ++l) sum += sums[(t * team + l) * d + x];
+        static_cast<T *>(p.k_mean)[pg_mean_elem(p.layer, slot_s[t] >> g.shift, h, g) + x] = from_f<T>(sum / ps);
       }
       __syncthreads();
     }
@@ -859,8 +867,8 @@ cudaError_t launch_rope_table(float2 *dst, int rows, int step, int head_dim, dou
 
 cudaError_t launch_pages_plan(const PlanParams &p, int sm_count, cudaStream_t st) {
   // A CTA's time is the scans over the requests: 1024 threads from 256 requests on (2000 requests and
-  // 91 thousand rows: 13.9 us, with 256 threads 17.1).  Two rows per thread: every CTA repeats the scans, so more of them only
-  // help until each SM has one.
+  // 91 thousand rows: 13.9 us, with 256 threads 17.1).  Two rows per thread: every CTA repeats the
+  // scans, so more of them only help until each SM has one.
   const bool many = p.batch > 256;
   const int threads = many ? 1024 : 256, want = (p.n_rows + 2 * threads - 1) / (2 * threads);
   const int ctas = want < 1 ? 1 : want < sm_count ? want : sm_count;
@@ -871,21 +879,25 @@ cudaError_t launch_pages_plan(const PlanParams &p, int sm_count, cudaStream_t st
 
 namespace {
 template <typename T, typename S>
-cudaError_t write(const WriteParams &p, cudaStream_t st) {
+cudaError_t write(const WriteParams &p, int sm_count, cudaStream_t st) {
   const int heads = p.n_q_heads + 2 * p.g.n_kv_heads;
   const long long items = (long long)p.n_rows * ((heads + HEADS - 1) / HEADS) * (p.g.head_dim / 16);
   const long long move = (items + WT - 1) / WT;
-  const int mean = p.k_mean ? (p.n_rows + MEAN_ROWS - 1) / MEAN_ROWS : 0;
-  k_pages_write<T, S><<<(unsigned)(move + mean), WT, 0, st>>>(p, mean);
+  // the means' CTAs search eight rows each, or more, so that at most MEAN_CTAS fall to an SM
+  int rows = 8;
+  while ((long long)((p.n_rows + rows - 1) / rows) * p.g.n_kv_heads > (long long)MEAN_CTAS * sm_count && rows < p.n_rows)
+    rows *= 2;
+  const int mean = p.k_mean ? (p.n_rows + rows - 1) / rows * p.g.n_kv_heads : 0;
+  k_pages_write<T, S><<<(unsigned)(move + mean), WT, 0, st>>>(p, mean, rows);
   return cudaGetLastError();
 }
 }  // namespace
 
-cudaError_t launch_pages_write(const WriteParams &p, int dtype, int src_dtype, cudaStream_t st) {
+cudaError_t launch_pages_write(const WriteParams &p, int dtype, int src_dtype, int sm_count, cudaStream_t st) {
   if (p.n_rows == 0) return cudaSuccess;
   const bool f32 = src_dtype == RTVLA_DTYPE_F32;
-  if (dtype == RTVLA_DTYPE_BF16) return f32 ? write<bf16, float>(p, st) : write<bf16, bf16>(p, st);
-  return f32 ? write<__half, float>(p, st) : write<__half, __half>(p, st);
+  if (dtype == RTVLA_DTYPE_BF16) return f32 ? write<bf16, float>(p, sm_count, st) : write<bf16, bf16>(p, sm_count, st);
+  return f32 ? write<__half, float>(p, sm_count, st) : write<__half, __half>(p, sm_count, st);
 }
 
 namespace {
@@ -893,7 +905,9 @@ size_t select_smem(const PageGeom &g) { return g.width <= SELECT_SMEM_KEYS ? (si
 
 template <typename T>
 cudaError_t select_attributes(int head_dim) {
-  const auto kernel = head_dim == 64 ? k_pages_select<T, 64> : head_dim == 128 ? k_pages_select<T, 128> : k_pages_select<T, 256>;
+  const auto kernel = head_dim == 64    ? k_pages_select<T, 64>
+                      : head_dim == 128 ? k_pages_select<T, 128>
+                                        : k_pages_select<T, 256>;
   return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, SELECT_SMEM_KEYS * 4);
 }
 

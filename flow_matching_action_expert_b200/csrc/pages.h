@@ -47,7 +47,7 @@ struct WriteParams {
   DevCtl *ctl;
 };
 // dtype: RTVLA_DTYPE_* of the cache and q_out; src_dtype: of the qkv rows
-cudaError_t launch_pages_write(const WriteParams &p, int dtype, int src_dtype, cudaStream_t st);
+cudaError_t launch_pages_write(const WriteParams &p, int dtype, int src_dtype, int sm_count, cudaStream_t st);
 
 struct PagedAttnParams {
   PageGeom g;

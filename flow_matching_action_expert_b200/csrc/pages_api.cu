@@ -235,7 +235,7 @@ rtvla_status rtvla_pages_write(rtvla_pages_ctx *c, int layer, const void *qkv, i
   if (!dev.ok) return RTVLA_ERR_CUDA;
   WriteParams p{c->g, layer, c->cfg.n_q_heads, n_rows, qkv,        slots,      positions,
                 kv->k, kv->v, kv->k_mean,      q_out,  c->rope_lo, c->rope_hi, c->ctl};
-  return launched(launch_pages_write(p, c->cfg.dtype, qkv_dtype, static_cast<cudaStream_t>(stream)));
+  return launched(launch_pages_write(p, c->cfg.dtype, qkv_dtype, c->sm_count, static_cast<cudaStream_t>(stream)));
 }
 
 rtvla_status rtvla_pages_attend(rtvla_pages_ctx *c, int layer, const void *q, const rtvla_paged_kv *kv,

@@ -512,7 +512,8 @@ rtvla_status rtvla_pages_create(const rtvla_pages_config *cfg, rtvla_pages_ctx *
  * number outside the pool (in the table or the free list) gives its rows slot -1 and reports the
  * same.  row_start counts every request's rows, refused ones too, up to n_rows.
  * A page may appear in several requests' tables (a shared prompt), but a request that shrinks must
- * not share what it gives back.  n_rows 0..2^24; slots and positions may be null when it is 0.  Errors: INVALID_ARG, SHAPE, CUDA.
+ * not share what it gives back.  n_rows 0..2^24; slots and positions may be null when it is 0.
+ * Errors: INVALID_ARG, SHAPE, CUDA.
  */
 rtvla_status rtvla_pages_plan(rtvla_pages_ctx *ctx, const int32_t *lens, const int32_t *delta,
                               int32_t *free_pages, const int32_t *n_free, const rtvla_paged_kv *kv,

@@ -62,7 +62,7 @@ class Cache:
         self.q = (torch.randn((len(lens), hq, d), generator=g, device="cuda") * std).to(self.t)
 
     def __del__(self):
-        if getattr(self, "ctx", 0):
+        if getattr(self, "ctx", 0) and R is not None and R.rtvla_pages_destroy is not None:
             R.rtvla_pages_destroy(self.ctx)
 
     def status(self):
@@ -281,9 +281,10 @@ def test_write_rows_pools_and_means(dtype, src, hq, hkv, d, page, theta):
     assert (got_q[~live] == float(torch.tensor(555.0).to(c.t))).all()  # the fill as the type holds it
     assert (np.abs(got_q - q) <= c.u * np.abs(q) + pair[:, :hq])[live].all()
     sl = torch.from_numpy(slots[live].astype(np.int64)).cuda()
-    for pool, old, ref, tol in ((c.k, before[0], k, pair[:, hq:hq + hkv]), (c.v, before[1], v, 2.0 ** -25 if c.f16 else 0.0)):
+    v_tol = np.full_like(pair[:, hq:hq + hkv], 2.0 ** -25 if c.f16 else 0.0)
+    for pool, old, ref, tol in ((c.k, before[0], k, pair[:, hq:hq + hkv]), (c.v, before[1], v, v_tol)):
         got = pool[1, sl // page, :, sl % page].double().cpu().numpy()
-        assert (np.abs(got - ref[live]) <= c.u * np.abs(ref[live]) + (tol[live] if hasattr(tol, "shape") else tol)).all()
+        assert (np.abs(got - ref[live]) <= c.u * np.abs(ref[live]) + tol[live]).all()
         old[1, sl // page, :, sl % page] = pool[1, sl // page, :, sl % page]
         assert torch.equal(pool.view(torch.int16), old.view(torch.int16))  # no other slot, no other layer
     full = sl[sl % page == page - 1] // page

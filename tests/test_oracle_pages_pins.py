@@ -63,8 +63,8 @@ def test_attention_matches_torch_on_shuffled_pages():
     assert not OP.attend_one(q, np.zeros((0, d)), np.zeros((0, d)))[0].any()
 
 
-@pytest.mark.parametrize("mistake", ["last key missing", "one key too many", "scale", "heads swapped", "page off by one",
-                                     "value of the next key"])
+@pytest.mark.parametrize("mistake", ["last key missing", "one key too many", "scale", "heads swapped",
+                                     "page off by one", "value of the next key"])
 @pytest.mark.parametrize("u, f16", [(2.0 ** -8, False), (2.0 ** -11, True)])
 def test_planted_mistakes_leave_the_attention_tolerance(mistake, u, f16):
     """Each mistake, made in the oracle, lands outside the bound the GPU tests use on 200 keys."""

@@ -885,8 +885,8 @@ cudaError_t write(const WriteParams &p, int sm_count, cudaStream_t st) {
   const long long move = (items + WT - 1) / WT;
   // the means' CTAs search eight rows each, or more, so that at most MEAN_CTAS fall to an SM
   int rows = 8;
-  while ((long long)((p.n_rows + rows - 1) / rows) * p.g.n_kv_heads > (long long)MEAN_CTAS * sm_count && rows < p.n_rows)
-    rows *= 2;
+  const long long most = (long long)MEAN_CTAS * sm_count;
+  while (rows < p.n_rows && (long long)((p.n_rows + rows - 1) / rows) * p.g.n_kv_heads > most) rows *= 2;
   const int mean = p.k_mean ? (p.n_rows + rows - 1) / rows * p.g.n_kv_heads : 0;
   k_pages_write<T, S><<<(unsigned)(move + mean), WT, 0, st>>>(p, mean, rows);
   return cudaGetLastError();

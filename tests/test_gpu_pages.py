@@ -140,6 +140,14 @@ def test_attend_with_lists_of_pages():
     c.check_attend(c.attend(sel=i32(sel)), picks=picks)
 
 
+def test_attend_with_pages_shared_by_requests():
+    # a prompt of 48 tokens in three requests' tables; the rest of each is its own
+    c = Cache([200, 100, 48, 75], hq=8, hkv=2, d=64, page=16)
+    c.table_np[1:, :3] = c.table_np[0, :3]
+    c.table.copy_(i32(c.table_np))
+    c.check_attend(c.attend())
+
+
 def test_attend_leaves_out_bad_pages_and_reports_them():
     c = Cache([64, 64, 64], page=16)
     bad = c.table_np.copy()
@@ -444,7 +452,7 @@ def test_steps_together_as_a_captured_graph():
         step(side)
     for i in range(20):
         if i == 7:
-            delta.copy_(i32([1, 1, -60, 1]))  # the third request drops its tail, then goes on
+            delta.copy_(i32([1, 1, -13, 1]))  # the third request drops the end of a full page, then refills it
         if i == 8:
             delta.copy_(i32([1, 1, 1, 1]))
         qkv.normal_()
@@ -461,6 +469,13 @@ def test_steps_together_as_a_captured_graph():
             picks = [[[e for e in row if e >= 0] for row in req] for req in sel[l].cpu().numpy()]
             c.check_attend(out[l], l, picks)
             c.check_attend(full[l], l)
+    # every full page's mean is that of the keys it holds now, pages filled a second time among them
+    for b, n in enumerate(c.lens_np):
+        pages = c.table_np[b, : n // 16].astype(np.int64)
+        for l in range(2):
+            keys = c.k[l, pages].double().cpu().numpy()
+            ref, got = keys.mean(2), c.k_mean[l, pages].double().cpu().numpy()
+            assert (np.abs(got - ref) <= c.u * np.abs(ref) + 16 * E32 * np.abs(keys).mean(2)).all()
 
 
 def test_contexts_on_two_streams_at_once():

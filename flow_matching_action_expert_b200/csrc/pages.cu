@@ -280,7 +280,7 @@ __device__ __forceinline__ void rotate8(float (&x1)[8], float (&x2)[8], const fl
 // its heads share through L1.  A thread takes eight pairs (16 bytes of each half) of HEADS heads.
 // Measured: 4348 rows of 10 heads of 256 (44 MB) 13 us, 3.4 TB/s: two waves of CTAs, each as long as
 // its chain of loads (slot, then table row); 9465 rows 23.6 us, 4.1 TB/s.  Two heads per thread take
-// 13.6 us; 64 registers instead of 80 spill (14.9).  A decode step of 16 rows: 4.9 us.
+// 13.6 us; 64 registers instead of 80 spill (14.9).  A decode step of 16 rows: 5.5 us.
 // The first CTAs look for rows that fill their page, one KV head each, several small pages at a time
 // (16 rows of 32 + 16 heads of 128: 3.8 us; with all heads and pages in turn 13.3).  The mean of such a page needs
 // the rows of this call that other CTAs write, so it is computed from their sources again; the page's
@@ -475,10 +475,10 @@ __device__ int scan_count(int v, int *warp_sums, int &total) {
 
 }  // namespace
 
-// One cluster per request and KV head.  The choice is defined by fp64 scores, but this GPU adds
-// fp64 numbers some ten times slower than fp32 ones (scoring 2040 pages of 256 components took
-// 12000 of 22000 cycles), so the cluster scores in fp32, 16 bytes of a page's mean per lane, and
-// puts order-preserving integer keys into the first CTA's shared memory.  An fp32 score is within
+// One cluster per request and KV head.  The choice is defined by fp64 scores, but fp64 sums are slow
+// (with them throughout, selection and attention of 64 of 2040 pages took 23.0 us instead of 21.5),
+// so the cluster scores in fp32, 16 bytes of a page's mean per lane, and puts order-preserving
+// integer keys into the first CTA's shared memory.  An fp32 score is within
 //   E = 16 * 2^-24 * sum_i |q_i| * max |mean|
 // of the exact one (8 products and sums in a lane, at most 5 sums over lanes, one rounding of q:
 // 14 roundings).  With t the `need`-th highest fp32 score, the `need`-th highest exact one lies
@@ -509,6 +509,7 @@ __global__ void __cluster_dims__(SC, 1, 1) __launch_bounds__(ST, 2) k_pages_sele
   const int rank = blockIdx.x, h = blockIdx.y, b = blockIdx.z, G = p.n_q_heads / g.n_kv_heads;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");  // the attention may be launched
+  asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");  // this CTA has started
   constexpr int LPP = D / 8, PPW = 32 / LPP;  // lanes per page, pages per load
   const int sub = lane / LPP, ln = lane % LPP;
   // the sum of the group's query heads, one component per thread; loads that need no length first
@@ -534,6 +535,9 @@ __global__ void __cluster_dims__(SC, 1, 1) __launch_bounds__(ST, 2) k_pages_sele
   const int held = pg_pages(pg_len(p.lens[b], g, &bad), g);
   if (bad && threadIdx.x == 0 && rank == 0 && h == 0) set_error(p.ctl, DEVERR_BOUNDS, PG_AT_SELECT);
   int *sel = p.sel + ((size_t)b * g.n_kv_heads + h) * p.budget;
+  // the first CTA's shared memory is written only once all of the cluster's CTAs have started
+  __syncwarp();
+  asm volatile("barrier.cluster.wait.aligned;" ::: "memory");
   if (held <= p.budget) {  // the whole cluster leaves here
     for (int i = rank * ST + threadIdx.x; i < p.budget; i += SC * ST) sel[i] = i < held ? i : -1;
     return;

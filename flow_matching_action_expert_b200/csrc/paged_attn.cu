@@ -29,8 +29,10 @@
 // takes 21 and the start, the last tiles and the join the rest.  Short calls are latency: 7.9 us
 // for one request of 544 tokens, 9.8 for 16 of 800.
 //
-// Weights are split into two 16-bit halves, p = hi + lo, and multiplied twice: the products cost
-// nothing next to the loads, and the weights then count to 2^-16 instead of 2^-8.
+// Weights are split into two 16-bit parts, p = hi + lo, and multiplied twice: the products cost
+// nothing next to the loads, and the weights then count to 2^-16 (bf16) or 2^-22 (f16) instead of
+// 2^-8 or 2^-11.  f16 has no numbers below 2^-24, so its parts are those of 2^15 p (at most 32768, of
+// 65504): what is lost of a small weight is at most 2^-40 of the largest.
 #include <cuda_fp16.h>
 
 #include <algorithm>
@@ -52,7 +54,11 @@ constexpr int CLUSTER = 8;      // CTAs that share a pair, when there are few pa
 __device__ __forceinline__ void put(bf16 *p, float v) { *p = __float2bfloat16_rn(v); }
 __device__ __forceinline__ void put(__half *p, float v) { *p = __float2half_rn(v); }
 
-// two values as (first in the low half) 16-bit hi parts and the 16-bit rest
+// two weights as (first in the low half) 16-bit hi parts and the 16-bit rest, of P_SCALE times each
+template <typename T>
+constexpr float P_SCALE = 1.f;
+template <>
+constexpr float P_SCALE<__half> = 32768.f;
 __device__ __forceinline__ void split2(float a, float b, uint32_t &hi, uint32_t &lo, bf16) {
   const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
   const __nv_bfloat162 l = __floats2bfloat162_rn(a - __low2float(h), b - __high2float(h));
@@ -60,6 +66,8 @@ __device__ __forceinline__ void split2(float a, float b, uint32_t &hi, uint32_t 
   lo = *reinterpret_cast<const uint32_t *>(&l);
 }
 __device__ __forceinline__ void split2(float a, float b, uint32_t &hi, uint32_t &lo, __half) {
+  a *= P_SCALE<__half>;
+  b *= P_SCALE<__half>;
   const __half2 h = __floats2half2_rn(a, b);
   const __half2 l = __floats2half2_rn(a - __low2float(h), b - __high2float(h));
   hi = *reinterpret_cast<const uint32_t *>(&h);
@@ -313,8 +321,8 @@ __device__ __forceinline__ void attend_chunks(const PagedAttnParams &p, uint8_t 
       if (gq == 0) ml_s[warp][head] = make_float2(m[nt][e], sum);
 #pragma unroll
       for (int i = 0; i < D / 16; ++i) {
-        so[head * S::OLD + 16 * i + gq] = o[i][nt][e];
-        so[head * S::OLD + 16 * i + gq + 8] = o[i][nt][e + 2];
+        so[head * S::OLD + 16 * i + gq] = o[i][nt][e] * (1.f / P_SCALE<T>);
+        so[head * S::OLD + 16 * i + gq + 8] = o[i][nt][e + 2] * (1.f / P_SCALE<T>);
       }
     }
   __syncthreads();

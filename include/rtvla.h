@@ -541,8 +541,9 @@ rtvla_status rtvla_pages_write(rtvla_pages_ctx *ctx, int layer, const void *qkv,
  * where it holds none.  q, out: device [batch][n_q_heads][head_dim] of the cache's dtype, 16-byte
  * aligned.  sel, if not null: device int32 [batch][n_kv_heads][sel_width], the logical pages
  * (0 .. pages held - 1) to attend to instead of all, the first min(sel_width, pages held) entries
- * used; a page listed twice counts twice.  Sums, maxima and weights are fp32; an infinite value
- * among those attended to gives NaN.  Nothing past a request's length is read.  A length past the
+ * used; a page listed twice counts twice.  Sums and maxima are fp32; a weight multiplies its value as
+ * two numbers of the cache's type, whose sum is within 2^-16 (bf16) or 2^-22 (f16) of it, relative, and
+ * in f16 2^-40 of the largest weight besides.  An infinite value among those attended to gives NaN.  Nothing past a request's length is read.  A length past the
  * table is clamped; keys of a page number outside the pool, or of a listed page that is not held,
  * are left out; each reports DEVICE_BOUNDS.  Errors: INVALID_ARG, SHAPE, CUDA.
  */

@@ -1,0 +1,75 @@
+"""The paged KV cache where one wrong step would hide at ordinary values: infinities, weights far below
+the maximum, page lists and bad pages in the split attention, many rows in one write, scores whose
+partial sums overflow.  Against the fp64 oracle.
+
+Tolerances: tests/pages_tolerances.py, without its term for small f16 weights (weight_tolerance).
+"""
+import numpy as np
+import pytest
+import torch
+
+from oracle import pages as OP
+
+from pages_tolerances import E32
+from test_gpu_pages import Cache
+
+pytestmark = pytest.mark.gpu
+
+
+def weight_tolerance(u, d, f16, ref, size, big, vv):
+    """As attend_tolerance, but an f16 weight p counts within 2^-22 p + 2^-40 of the largest: two parts of
+    11 bits (2^-11 * 2^-11), the first of the weight times 2^15, so that half a step of the smallest
+    numbers, 2^-25, is 2^-40.  (bf16: two parts of 8 bits, 2^-16 p, no smallest step that matters.)"""
+    n = len(vv)
+    tol = u * np.abs(ref) + (2 * (d + 4) * E32 * big + (2 * n + 136) * E32 + 2.0 ** (-22 if f16 else -16)) * size
+    if f16:
+        tol = tol + 2.0 ** -25 + n * 2.0 ** -40 * (np.abs(vv).max() if n else 0.0)
+    return tol
+
+
+class Tight(Cache):
+    def close(self, got, ref, size, big, kk, vv, what):
+        tol = weight_tolerance(self.u, self.d, self.f16, ref, size, big, vv)
+        err = np.abs(got - ref)
+        assert np.isfinite(got).all() and (err <= tol).all(), (what, float((err - tol).max()))
+        if len(kk) == 0:
+            assert not got.any()
+
+
+ROOMS = [None, 8192]  # table rows with room for 8192 tokens make one request go to the split attention
+
+
+def roomy(room, page):
+    return room and OP.pages_for(room, page)
+
+
+# ---------------------------------------------------------------------------------------
+# attention
+
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+@pytest.mark.parametrize("room", ROOMS)
+@pytest.mark.parametrize("nats", [12.0, 16.0, 18.0, 22.0])
+def test_attend_long_tail_of_small_weights(dtype, room, nats):
+    """One dominant key in every 16, the others `nats` below it (18: 2^-26), which alone have values: their
+    sum, 15000 e^-nats, is what the output is made of."""
+    c = Tight([1024], dtype, hq=1, d=64, width=roomy(room, 16))
+    at = torch.zeros((1024, 64), dtype=c.t, device="cuda")
+    at[:, 0] = -nats
+    at[::16, 0] = 0.0
+    pages = c.table[0, :64].long()
+    c.k[0, pages, 0] = at.view(64, 16, 64)
+    at[:] = 1000.0
+    at[::16] = 0.0
+    c.v[0, pages, 0] = at.view(64, 16, 64)
+    c.q.zero_()
+    c.q[0, 0, 0] = 8.0  # logits are the keys' first component
+    c.check_attend(c.attend())
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+@pytest.mark.parametrize("hq, hkv, d", [(8, 1, 256), (16, 1, 64), (8, 2, 128)])
+@pytest.mark.parametrize("room", ROOMS)
+@pytest.mark.parametrize("std", [1.0, 3.0])
+def test_attend_to_the_weights_own_precision(dtype, hq, hkv, d, room, std):
+    c = Tight([1000, 17, 333], dtype, hq, hkv, d, width=roomy(room, 16), std=std)
+    c.check_attend(c.attend())

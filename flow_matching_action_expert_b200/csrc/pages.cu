@@ -481,9 +481,10 @@ __device__ int scan_count(int v, int *warp_sums, int &total) {
 // integer keys into the first CTA's shared memory.  An fp32 score is within
 //   E = 16 * 2^-24 * sum_i |q_i| * max |mean|
 // of the exact one (8 products and sums in a lane, at most 5 sums over lanes, one rounding of q:
-// 14 roundings).  With t the `need`-th highest fp32 score, the `need`-th highest exact one lies
-// within E of t: pages above t + 2E are in, pages below t - 2E are out, and only those between are
-// scored again in fp64 - with ordinary scores the page at t alone.
+// 14 roundings); where an fp32 sum is not finite, though the exact one may be, E counts as infinite.
+// With t the `need`-th highest fp32 score, the `need`-th highest exact one lies within E of t: pages
+// above t + 2E are in, pages below t - 2E are out, and only those between are scored again in fp64 -
+// with ordinary scores the page at t alone.
 //
 // t is found by one histogram over equal steps of the score and a comparison of all pairs in the
 // deciding step; where that step holds too many (or a bound is not finite), radix passes over the
@@ -593,7 +594,6 @@ __global__ void __cluster_dims__(SC, 1, 1) __launch_bounds__(ST, 2) k_pages_sele
             s[i] = fmaf(q[u + 1], f[u + 1], s[i]);
             big = fmaxf(big, fmaxf(fabsf(f[u]), fabsf(f[u + 1])));
           }
-          if (!(fabsf(s[i]) < INFINITY)) big = INFINITY;  // no bound: all pages go by fp64
         }
         // sums over the LPP lanes of a page; the first steps halve the pages a lane holds
         int i = 0;
@@ -611,6 +611,7 @@ __global__ void __cluster_dims__(SC, 1, 1) __launch_bounds__(ST, 2) k_pages_sele
             s[0] += __shfl_xor_sync(0xffffffffu, s[0], o);
           }
         }
+        if (!(fabsf(s[0]) < INFINITY)) big = INFINITY;  // no bound: all pages go by fp64
         const int at = i0 + i * PPW + sub, page = __shfl_sync(0xffffffffu, mine, at);
         if (!(lane & (LPP / LOADS - 1)) && c0 + at < n) dst[(c0 + at) * ks] = page < 0 ? 0 : key32(s[0]);
       }

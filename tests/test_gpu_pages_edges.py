@@ -8,10 +8,11 @@ import numpy as np
 import pytest
 import torch
 
+import flow_matching_action_expert_b200 as R
 from oracle import pages as OP
 
 from pages_tolerances import E32
-from test_gpu_pages import Cache
+from test_gpu_pages import Cache, check_select
 
 pytestmark = pytest.mark.gpu
 
@@ -73,3 +74,25 @@ def test_attend_long_tail_of_small_weights(dtype, room, nats):
 def test_attend_to_the_weights_own_precision(dtype, hq, hkv, d, room, std):
     c = Tight([1000, 17, 333], dtype, hq, hkv, d, width=roomy(room, 16), std=std)
     c.check_attend(c.attend())
+
+
+# ---------------------------------------------------------------------------------------
+# selection
+
+def test_select_with_partial_sums_that_overflow():
+    """Scores that are ordinary numbers but whose fp32 sums pass through infinity."""
+    c = Cache([16 * 200], page=16, d=64, hq=1)
+    c.q.fill_(1.0)
+    m = c.k_mean[0, :, 0]
+    pages = c.table[0].long()
+    big = torch.zeros((3, 8, 8), device="cuda")   # eight components to a block
+    big[0, [0, 4]], big[0, [1, 5]] = 4e37, -4e37   # + and - infinity on the way; the score is 0
+    big[1, 0], big[1, 4] = -4e37, -4e37            # -infinity on the way; the score is 2e37 or so
+    big[1, [1, 3]], big[1, 2] = 2.06e37, 4.12e37
+    big[2, [0, 4]], big[2, [1, 3]], big[2, 2] = 4e37, -2.06e37, -4.12e37  # +infinity; the score is -2e37 or so
+    m[pages[[20, 60, 110]]] = big.view(3, 64).to(c.t)
+    for budget in (2, 30, 199):
+        sel = torch.empty((1, 1, budget), dtype=torch.int32, device="cuda")
+        R.rtvla_pages_select(c.ctx, 0, c.q, c.kv, budget, 0, 1, sel)
+        assert c.status() == "RTVLA_OK"
+        check_select(c, sel, budget, 0, 1)

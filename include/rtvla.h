@@ -543,9 +543,12 @@ rtvla_status rtvla_pages_write(rtvla_pages_ctx *ctx, int layer, const void *qkv,
  * (0 .. pages held - 1) to attend to instead of all, the first min(sel_width, pages held) entries
  * used; a page listed twice counts twice.  Sums and maxima are fp32; a weight multiplies its value as
  * two numbers of the cache's type, whose sum is within 2^-16 (bf16) or 2^-22 (f16) of it, relative, and
- * in f16 2^-40 of the largest weight besides.  An infinite value among those attended to gives NaN.  Nothing past a request's length is read.  A length past the
- * table is clamped; keys of a page number outside the pool, or of a listed page that is not held,
- * are left out; each reports DEVICE_BOUNDS.  Errors: INVALID_ARG, SHAPE, CUDA.
+ * in f16 2^-40 of the largest weight besides.  A key whose logit is -infinity has weight 0 (if all are,
+ * the output is 0); a logit that is +infinity or NaN makes its query head's output NaN; a value that is
+ * not finite makes its component of the output NaN or infinite, unless its weight is 0: then it may or
+ * may not.  No other head, component or request changes.  Nothing past a request's length is read.  A
+ * length past the table is clamped; keys of a page number outside the pool, or of a listed page that is
+ * not held, are left out; each reports DEVICE_BOUNDS.  Errors: INVALID_ARG, SHAPE, CUDA.
  */
 rtvla_status rtvla_pages_attend(rtvla_pages_ctx *ctx, int layer, const void *q, const rtvla_paged_kv *kv,
                                 const int32_t *sel, int sel_width, void *out, void *stream);
@@ -557,9 +560,9 @@ rtvla_status rtvla_pages_attend(rtvla_pages_ctx *ctx, int layer, const void *q, 
  * of the others those with the highest score (sum of the KV head's query heads) . k_mean[page],
  * equal scores by lower page number.  The products are exact and their sum is fp64, so the choice
  * does not depend on the order of summation short of fp64 rounding.  keep_first >= 0, keep_last >= 1,
- * keep_first + keep_last <= budget <= 65536.  A page number outside the pool scores below every
- * other page and reports DEVICE_BOUNDS.  Errors: INVALID_ARG (k_mean null), SHAPE, UNSUPPORTED
- * (has_select 0), CUDA.
+ * keep_first + keep_last <= budget <= 65536.  Scores may be infinite; where a NaN score ranks is
+ * unspecified.  A page number outside the pool scores below every other page and reports
+ * DEVICE_BOUNDS.  Errors: INVALID_ARG (k_mean null), SHAPE, UNSUPPORTED (has_select 0), CUDA.
  */
 rtvla_status rtvla_pages_select(rtvla_pages_ctx *ctx, int layer, const void *q, const rtvla_paged_kv *kv,
                                 int budget, int keep_first, int keep_last, int32_t *sel, void *stream);

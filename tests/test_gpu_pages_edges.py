@@ -76,6 +76,49 @@ def test_attend_to_the_weights_own_precision(dtype, hq, hkv, d, room, std):
     c.check_attend(c.attend())
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+@pytest.mark.parametrize("room", ROOMS)
+def test_attend_with_infinities(dtype, room):
+    """Logits of -inf have weight 0, of +inf or NaN make their head NaN, values that are not finite make
+    their component so; nothing else changes."""
+    inf = float("inf")
+    c = Tight([500, 40, 300, 300], dtype, hq=4, hkv=1, d=64, width=roomy(room, 16))
+    c.q[:, :, 0] = torch.tensor([1.0, 0.5, 2.0, -1.0], device="cuda", dtype=c.t)
+    gone = [3, 16, 17, 18, 19, 200, 499]
+    page, off = [int(c.table_np[0, j // 16]) for j in gone], [j % 16 for j in gone]
+    c.k[0, page, 0, off, 0] = -inf                          # -inf for heads 0 to 2, +inf for head 3
+    c.k[0, c.table[1, :3].long(), 0, :, 0] = -inf           # every key of the second request
+    p = int(c.table_np[2, 7])
+    c.v[0, p, 0, 5, 9], c.v[0, p, 0, 6, 11], c.v[0, p, 0, 7, 13] = inf, -inf, float("nan")
+    c.k[0, int(c.table_np[3, 2]), 0, 1, 30] = float("nan")
+    out = c.attend().double().cpu().numpy()
+    k, v, q = (x.double().cpu().numpy() for x in (c.k[0], c.v[0], c.q))
+    keep = [j for j in range(500) if j not in gone]
+    kk, vv = (OP.keys_of(x, c.table_np[0], 500, 0, 16)[keep] for x in (k, v))
+    ref, size, big = OP.attend_one(q[0, :3], kk, vv)
+    assert (np.abs(out[0, :3] - ref) <= weight_tolerance(c.u, 64, c.f16, ref, size, big, vv)).all()
+    assert np.isnan(out[0, 3]).all()
+    assert not out[1, :3].any() and np.isnan(out[1, 3]).all()
+    off = [9, 11, 13]
+    rest = [i for i in range(64) if i not in off]
+    kk, vv = (OP.keys_of(x, c.table_np[2], 300, 0, 16) for x in (k, v))
+    ref, size, big = OP.attend_one(q[2], kk, vv[:, rest])
+    assert (np.abs(out[2][:, rest] - ref) <= weight_tolerance(c.u, 64, c.f16, ref, size, big, vv[:, rest])).all()
+    assert not np.isfinite(out[2][:, off]).any()
+    assert np.isnan(out[3]).all()
+
+
+@pytest.mark.parametrize("room", ROOMS)
+def test_attend_with_a_queries_infinity(room):
+    c = Tight([100, 100], hq=2, d=64, width=roomy(room, 16))
+    c.q[0, 1, 4] = float("inf")
+    out = c.attend()
+    assert out[0, 1].isnan().all()
+    c.q[0, 1] = 0.0
+    clean = c.attend()
+    assert torch.equal(out[0, 0], clean[0, 0]) and torch.equal(out[1], clean[1])
+
+
 # ---------------------------------------------------------------------------------------
 # selection
 

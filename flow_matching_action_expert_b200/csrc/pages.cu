@@ -162,7 +162,11 @@ __global__ void __launch_bounds__(PT) k_pages_plan(PlanParams p) {
     const int b = owner(s_take, B, i);
     p.table[(size_t)b * g.width + pg_pages(s_len[b], g) + (i - s_take[b])] = popped(i);
   }
-  for (int e = first; e < n_back; e += stride) p.free_pages[nf + e] = given_back(e);
+  for (int e = first; e < n_back; e += stride) {
+    const int page = given_back(e);
+    bad |= page < 0 || page >= g.n_pages;
+    p.free_pages[nf + e] = page;
+  }
   for (int r = first; r < p.n_rows; r += stride) {
     int slot = -1, pos = 0;
     if (r < s_rows[B]) {

@@ -508,9 +508,10 @@ rtvla_status rtvla_pages_create(const rtvla_pages_config *cfg, rtvla_pages_ctx *
  * kv->k, kv->v and kv->k_mean are not used.  A request whose new pages do not fit in what is free
  * is refused, and with it every later request that needs pages: it keeps its length, its rows get
  * slot -1, and rtvla_pages_sync_status reports NO_PAGES.  A length outside its range, tokens past
- * table_width pages or rows past n_rows refuse that request alone and report DEVICE_BOUNDS; a page
- * number outside the pool (in the table or the free list) gives its rows slot -1 and reports the
- * same.  row_start counts every request's rows, refused ones too, up to n_rows.
+ * table_width pages or rows past n_rows refuse that request alone (its new length is the old one, a
+ * length outside its range clamped to it) and report DEVICE_BOUNDS; a page number outside the pool
+ * (in the table or the free list) gives its rows slot -1, is pushed as it stands if given back, and
+ * reports the same.  row_start counts every request's rows, refused ones too, up to n_rows.
  * A page may appear in several requests' tables (a shared prompt), but a request that shrinks must
  * not share what it gives back.  n_rows 0..2^24; slots and positions may be null when it is 0.
  * Errors: INVALID_ARG, SHAPE, CUDA.
@@ -585,7 +586,8 @@ rtvla_status rtvla_pages_select(rtvla_pages_ctx *ctx, int layer, const void *q, 
 rtvla_status rtvla_prefix_step(rtvla_ctx *ctx, rtvla_pages_ctx *pages, const void *embeds, const int32_t *slots,
                                const int32_t *positions, const rtvla_paged_kv *kv, float *hidden, void *stream);
 
-/* As rtvla_sync_status, for a paged-cache context (NO_PAGES, DEVICE_BOUNDS, GUARD_OVERWRITE). */
+/* As rtvla_sync_status, for a paged-cache context; of several errors since the last call the first of
+ * GUARD_OVERWRITE, DEVICE_BOUNDS, NO_PAGES. */
 rtvla_status rtvla_pages_sync_status(rtvla_pages_ctx *ctx, void *stream);
 
 /* Frees everything the context owns (waits for the device first).  NULL is a no-op. */

@@ -41,6 +41,8 @@ def plan(lens, delta, table, free_pages, n_free, page, n_pages, n_rows):
     after = [n if a else max(n + d, 0) for n, d, a in zip(lens, delta, alone)]
     for b, (n, m) in enumerate(zip(lens, after)):
         for i in range(pages_for(m, page), pages_for(n, page)):
+            if not 0 <= table[b, i] < n_pages:  # pushed as it stands
+                err.add("bounds")
             free[nf] = table[b, i]
             nf += 1
     slots, positions = np.full(n_rows, -1, np.int32), np.zeros(n_rows, np.int32)

@@ -12,7 +12,7 @@ import flow_matching_action_expert_b200 as R
 from oracle import pages as OP
 
 from pages_tolerances import E32
-from test_gpu_pages import Cache, check_select, i32
+from test_gpu_pages import Cache, check_select, i32, run_plan
 
 pytestmark = pytest.mark.gpu
 
@@ -263,3 +263,15 @@ def test_select_with_partial_sums_that_overflow():
         R.rtvla_pages_select(c.ctx, 0, c.q, c.kv, budget, 0, 1, sel)
         assert c.status() == "RTVLA_OK"
         check_select(c, sel, budget, 0, 1)
+
+
+# ---------------------------------------------------------------------------------------
+# plan and write
+
+def test_plan_reports_a_bad_page_given_back():
+    c = Cache([40, 64], d=64, hq=1, page=16)
+    c.table_np[0, 2] = c.n_pages + 3
+    assert "bounds" in run_plan(c, [40, 64], [-20, 0], 4)["err"]
+    c.table_np[0, 2] = -1
+    assert "bounds" in run_plan(c, [40, 64], [-40, 0], 4)["err"]
+    assert not run_plan(c, [40, 64], [-7, 0], 4)["err"]  # the request keeps it

@@ -368,10 +368,10 @@ __global__ void __launch_bounds__(WT) k_pages_write(WriteParams p, int mean_ctas
 #pragma unroll 2
         for (int o = lane_r % team; o < ps; o += team) {
           float x1[8], x2[8];
-          // the key `back` tokens before: of this call's row as far before, if that has its slot
-          const int back = ps - 1 - o, row = r - back;
-          if (row >= 0 && p.slots[row] == slot - back) {
-            const int pos = min(max(p.positions[row], 0), cap - 1);
+          // the key `back` tokens before: of this call's row as far before, if that has its slot and is
+          // written there (its position may be none)
+          const int back = ps - 1 - o, row = r - back, pos = row >= 0 ? p.positions[row] : -1;
+          if (pos >= 0 && pos < cap && p.slots[row] == slot - back) {
             const S *x = src + row * ld + (size_t)(hq + h) * d + i8 * 8;
             load8(x1, x);
             load8(x2, x + half);

@@ -275,3 +275,22 @@ def test_plan_reports_a_bad_page_given_back():
     c.table_np[0, 2] = -1
     assert "bounds" in run_plan(c, [40, 64], [-40, 0], 4)["err"]
     assert not run_plan(c, [40, 64], [-7, 0], 4)["err"]  # the request keeps it
+
+
+@pytest.mark.parametrize("page, bad_row", [(4, 1), (16, 0), (16, 14)])
+def test_mean_of_a_page_with_a_skipped_row(page, bad_row):
+    """A row whose position is none is skipped; its page's mean is of the key that is stored there."""
+    c = Cache([2 * page], d=64, hq=1, page=page, width=4)
+    p = int(c.table_np[0, 1])
+    slots, pos = p * page + np.arange(page), page + np.arange(page)
+    pos[bad_row] = -5 if bad_row else 4 * page
+    q_out = torch.zeros((page, 1, 64), dtype=c.t, device="cuda")
+    kept = c.k[0, p, 0, bad_row].clone()
+    R.rtvla_pages_write(c.ctx, 0, torch.randn((page, 192), device="cuda"), R.DTYPE_F32, i32(slots), i32(pos), page,
+                        c.kv, q_out)
+    assert c.status() == "RTVLA_ERR_DEVICE_BOUNDS"
+    assert torch.equal(c.k[0, p, 0, bad_row], kept)
+    stored = c.k[0, p, 0].double()
+    ref = stored.mean(0)
+    assert ((c.k_mean[0, p, 0].double() - ref).abs()
+            <= c.u * ref.abs() + page * E32 * stored.abs().mean(0)).all()

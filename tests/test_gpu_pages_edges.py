@@ -277,6 +277,61 @@ def test_plan_reports_a_bad_page_given_back():
     assert not run_plan(c, [40, 64], [-7, 0], 4)["err"]  # the request keeps it
 
 
+def _write_long(c, lens, new, pad, src, layer=0):
+    ref = OP.plan(lens, new, c.table_np, c.free_np, c.n_free, c.page, c.n_pages, int(sum(new)))
+    assert not ref["err"]
+    rng = np.random.default_rng(31)
+    T = int(sum(new)) + pad
+    # skipped rows only between requests: a page's rows follow one another
+    req = np.repeat(np.arange(len(new)), new)
+    gap = np.sort(rng.choice(len(new) + 1, pad)) if pad else np.zeros(0, int)
+    at = np.arange(T - pad) + np.searchsorted(gap, req, side="right")
+    slots, pos = np.full(T, -1, np.int32), np.zeros(T, np.int32)
+    slots[at], pos[at] = ref["slots"], ref["positions"]
+    qkv = torch.randn((T, (c.hq + 2 * c.hkv) * c.d), device="cuda")
+    qkv = qkv if src == "f32" else qkv.to(c.t)
+    code = R.DTYPE_F32 if src == "f32" else c.cfg.dtype
+    q_out = torch.full((T, c.hq, c.d), 555.0, dtype=c.t, device="cuda")
+    before = c.k_mean.clone()
+    R.rtvla_pages_write(c.ctx, layer, qkv, code, i32(slots), i32(pos), T, c.kv, q_out)
+    assert c.status() == "RTVLA_OK"
+    return slots, pos, qkv, q_out, before
+
+
+@pytest.mark.parametrize("dtype, src, hq, hkv, page, lens, new, pad", [
+    # a CTA looks for full pages in 16 rows, in 64, in 256, in 512
+    ("bf16", "f32", 1, 1, 2, [0, 5, 100, 63], [1500, 1, 1409, 90], 1),
+    ("f16", "same", 4, 4, 16, [7, 0, 300], [1000, 17, 2002], 40),
+    ("bf16", "same", 4, 4, 4, [3, 0, 17, 1], [5003, 1, 4000, 3300], 57),
+    ("f16", "f32", 8, 8, 1, [0, 9], [9000, 3001], 3),
+    ("bf16", "f32", 2, 2, 128, [100, 1], [11000, 127], 0)])
+def test_write_of_thousands_of_rows(dtype, src, hq, hkv, page, lens, new, pad):
+    need = sum(OP.pages_for(n + m, page) - OP.pages_for(n, page) for n, m in zip(lens, new))
+    c = Cache(lens, dtype, hq, hkv, 64, page, width=OP.pages_for(12000, page), spare=need + 3)
+    slots, pos, qkv, q_out, before = _write_long(c, lens, new, pad, src)
+    live = torch.from_numpy(slots >= 0).cuda()
+    sl = torch.from_numpy(slots[slots >= 0].astype(np.int64)).cuda()
+    full = sl[sl % page == page - 1] // page
+    stored = c.k[0, full].double()
+    ref, got = stored.mean(2), c.k_mean[0, full].double()
+    tol = c.u * ref.abs() + page * E32 * stored.abs().mean(2) + (2.0 ** -25 if c.f16 else 0.0)
+    assert len(full) and ((got - ref).abs() <= tol).all()
+    before[0, full] = c.k_mean[0, full]
+    assert torch.equal(c.k_mean.view(torch.int16), before.view(torch.int16))  # no other page's mean
+    # rows against the formula, in fp64 on the GPU
+    x = qkv.double().view(len(slots), hq + 2 * hkv, 64)
+    freq = 10000.0 ** (-torch.arange(32, dtype=torch.float64, device="cuda") / 32)
+    ang = torch.from_numpy(pos).cuda().double()[:, None, None] * freq
+    x1, x2 = x[:, :hq + hkv, :32], x[:, :hq + hkv, 32:]
+    y = torch.cat((x1 * ang.cos() - x2 * ang.sin(), x2 * ang.cos() + x1 * ang.sin()), -1)
+    tol = 8 * E32 * torch.cat([x1.abs() + x2.abs()] * 2, -1) + c.u * y.abs() + (2.0 ** -25 if c.f16 else 0.0)
+    assert ((q_out.double() - y[:, :hq]).abs() <= tol[:, :hq])[live].all()
+    assert (q_out[~live] == float(torch.tensor(555.0).to(c.t))).all()
+    k, v = (t[0, sl // page, :, sl % page] for t in (c.k, c.v))
+    assert ((k.double() - y[live, hq:]).abs() <= tol[live, hq:]).all()
+    assert torch.equal(v, x[live, hq + hkv:].to(c.t))
+
+
 @pytest.mark.parametrize("page, bad_row", [(4, 1), (16, 0), (16, 14)])
 def test_mean_of_a_page_with_a_skipped_row(page, bad_row):
     """A row whose position is none is skipped; its page's mean is of the key that is stored there."""

@@ -284,11 +284,12 @@ __device__ __forceinline__ void rotate8(float (&x1)[8], float (&x2)[8], const fl
 // its heads share through L1.  A thread takes eight pairs (16 bytes of each half) of HEADS heads.
 // Measured: 4348 rows of 10 heads of 256 (44 MB) 13 us, 3.4 TB/s: two waves of CTAs, each as long as
 // its chain of loads (slot, then table row); 9465 rows 23.6 us, 4.1 TB/s.  Two heads per thread take
-// 13.6 us; 64 registers instead of 80 spill (14.9).  A decode step of 16 rows: 5.5 us.
-// The first CTAs look for rows that fill their page, one KV head each, several small pages at a time
-// (16 rows of 32 + 16 heads of 128: 3.8 us; with all heads and pages in turn 13.3).  The mean of such a page needs
-// the rows of this call that other CTAs write, so it is computed from their sources again; the page's
-// earlier keys come from the pool.
+// 13.6 us; 64 registers instead of 80 spill (14.9).  A decode step of 16 rows: 4.3 us.
+// The first CTAs look for rows that fill their page, one KV head each, several small pages at a time; a
+// CTA's further pages follow one another, at 1.7 us each, so it takes as few rows as the grid allows (16
+// rows that fill four pages of 16: 3.3 us, with eight rows to a CTA 8.6; 32 + 16 heads of 128: 3.5, with
+// all heads and pages in turn 78).  The mean of such a page needs the rows of this call that other CTAs
+// write, so it is computed from their sources again; the page's earlier keys come from the pool.
 template <typename T, typename S>
 __global__ void __launch_bounds__(WT) k_pages_write(WriteParams p, int mean_ctas, int mean_rows) {
   const PageGeom g = p.g;
@@ -892,8 +893,9 @@ cudaError_t write(const WriteParams &p, int sm_count, cudaStream_t st) {
   const int heads = p.n_q_heads + 2 * p.g.n_kv_heads;
   const long long items = (long long)p.n_rows * ((heads + HEADS - 1) / HEADS) * (p.g.head_dim / 16);
   const long long move = (items + WT - 1) / WT;
-  // the means' CTAs search eight rows each, or more, so that at most MEAN_CTAS fall to an SM
-  int rows = 8;
+  // the means' CTAs search one row each, or as many (a power of two) as let at most MEAN_CTAS fall to an SM
+  // (one per SM: 4348 rows 13.9 -> 15.1 us, 2365 rows 9.6 -> 9.0)
+  int rows = 1;
   const long long most = (long long)MEAN_CTAS * sm_count;
   while (rows < p.n_rows && (long long)((p.n_rows + rows - 1) / rows) * p.g.n_kv_heads > most) rows *= 2;
   const int mean = p.k_mean ? (p.n_rows + rows - 1) / rows * p.g.n_kv_heads : 0;

@@ -327,6 +327,25 @@ cudaError_t enqueue_denoise(rtvla_ctx *c, const CallArgs *dargs, int B, int cap,
   return cudaSuccess;
 }
 
+// The second half of a prefix layer for M rows: output projection, norm and gated-GELU MLP, added to px.
+cudaError_t enqueue_pf_mlp(rtvla_ctx *c, int l, int M, bool glu, cudaStream_t st, int *kernels) {
+  int n = 0;
+  CKN(gemm_launch(c->tm_pwo, l * DP, c->tm_po, M, DP, NQH * HD, c->px, c->tmo_px, DP, nullptr, true, c->ctl,
+                  c->sm_count, st));
+  CKN(launch_rmsnorm(c->px, c->pop, M, DP, c->cfg.rms_eps, st));
+  if (glu) {
+    CKN(gemm_launch_glu(c->tm_pwgu64, l * 2 * FP, c->tm_pop, M, FP, DP, c->tm_pmb.m[0], nullptr, nullptr, c->ctl,
+                        c->sm_count, st));
+  } else {
+    CKN(gemm_launch(c->tm_pwgu, l * 2 * FP, c->tm_pop, M, 2 * FP, DP, c->pacc, c->tmo_pgu, 2 * FP, nullptr, false,
+                    c->ctl, c->sm_count, st));
+    CKN(launch_gelu_mul(c->pacc, nullptr, nullptr, c->pmb, M, FP, st));
+  }
+  CKN(gemm_launch(c->tm_pwd, l * DP, c->tm_pmb, M, DP, FP, c->px, c->tmo_px, DP, nullptr, true, c->ctl, c->sm_count, st));
+  *kernels += n;
+  return cudaSuccess;
+}
+
 cudaError_t enqueue_prefill(rtvla_ctx *c, const CallArgs *dargs, int B, int P, cudaStream_t st, int *kernels) {
   int n = 0;
   const int L = c->L, M = B * P;
@@ -359,18 +378,7 @@ cudaError_t enqueue_prefill(rtvla_ctx *c, const CallArgs *dargs, int B, int P, c
     ap.layer = l;
     CKN(attn_launch(ap, B, st));
     if (ap.n_splits > 1) ++n;
-    CKN(gemm_launch(c->tm_pwo, l * DP, c->tm_po, M, DP, NQH * HD, c->px, c->tmo_px, DP, nullptr, true, c->ctl,
-                    c->sm_count, st));
-    CKN(launch_rmsnorm(c->px, c->pop, M, DP, eps, st));
-    if (glu) {
-      CKN(gemm_launch_glu(c->tm_pwgu64, l * 2 * FP, c->tm_pop, M, FP, DP, c->tm_pmb.m[0], nullptr, nullptr, c->ctl,
-                          c->sm_count, st));
-    } else {
-      CKN(gemm_launch(c->tm_pwgu, l * 2 * FP, c->tm_pop, M, 2 * FP, DP, c->pacc, c->tmo_pgu, 2 * FP, nullptr, false,
-                      c->ctl, c->sm_count, st));
-      CKN(launch_gelu_mul(c->pacc, nullptr, nullptr, c->pmb, M, FP, st));
-    }
-    CKN(gemm_launch(c->tm_pwd, l * DP, c->tm_pmb, M, DP, FP, c->px, c->tmo_px, DP, nullptr, true, c->ctl, c->sm_count, st));
+    CKR(enqueue_pf_mlp(c, l, M, glu, st, &n));
   }
   *kernels = n;
   return cudaSuccess;
@@ -1148,10 +1156,11 @@ static rtvla_status prefix_step(rtvla_ctx *c, rtvla_pages_ctx *pages, const void
       return RTVLA_ERR_CUDA;                      \
     }                                             \
   } while (0)
+  int n = 0;
   const int M = kv->batch;
   const float eps = c->cfg.rms_eps;
   const bool glu = gemm_glu_applies(M, FP, DP, c->sm_count);
-  // the accumulator starts at zero for both GEMMs that use it
+  // the accumulators start at zero, as in enqueue_prefill
   CKS(cudaMemsetAsync(c->pacc, 0, (size_t)M * (glu ? 2560 : 2 * FP) * 4, st));
   CKS(launch_scale_to_f32(static_cast<const bf16 *>(embeds), M * DP, 1.0, c->px, st));
   for (int l = 0; l < c->L; ++l) {
@@ -1162,18 +1171,7 @@ static rtvla_status prefix_step(rtvla_ctx *c, rtvla_pages_ctx *pages, const void
     if (s == RTVLA_OK) s = rtvla_pages_attend(pages, l, c->pq, kv, nullptr, 0, c->po, st);
     if (s != RTVLA_OK) return s;
     CKS(cudaMemsetAsync(c->pacc, 0, (size_t)M * 2560 * 4, st));
-    CKS(gemm_launch(c->tm_pwo, l * DP, c->tm_po, M, DP, NQH * HD, c->px, c->tmo_px, DP, nullptr, true, c->ctl,
-                    c->sm_count, st));
-    CKS(launch_rmsnorm(c->px, c->pop, M, DP, eps, st));
-    if (glu) {
-      CKS(gemm_launch_glu(c->tm_pwgu64, l * 2 * FP, c->tm_pop, M, FP, DP, c->tm_pmb.m[0], nullptr, nullptr, c->ctl,
-                          c->sm_count, st));
-    } else {
-      CKS(gemm_launch(c->tm_pwgu, l * 2 * FP, c->tm_pop, M, 2 * FP, DP, c->pacc, c->tmo_pgu, 2 * FP, nullptr, false,
-                      c->ctl, c->sm_count, st));
-      CKS(launch_gelu_mul(c->pacc, nullptr, nullptr, c->pmb, M, FP, st));
-    }
-    CKS(gemm_launch(c->tm_pwd, l * DP, c->tm_pmb, M, DP, FP, c->px, c->tmo_px, DP, nullptr, true, c->ctl, c->sm_count, st));
+    CKS(enqueue_pf_mlp(c, l, M, glu, st, &n));
   }
   CKS(cudaMemcpyAsync(hidden, c->px, (size_t)M * DP * 4, cudaMemcpyDeviceToDevice, st));
 #undef CKS

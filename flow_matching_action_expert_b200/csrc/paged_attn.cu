@@ -410,7 +410,7 @@ __global__ void __launch_bounds__(WARPS * 32, ctas_per_sm<D, NT>()) k_pages_atte
   }
   total *= g.n_kv_heads;
   before *= g.n_kv_heads;
-  const long long ctas = min(total, (long long)gridDim.x);  // those with work: every range holds a chunk
+  const long long ctas = min(total, (long long)gridDim.x);  // those with work: every range holds a unit
   if (blockIdx.x >= ctas) return;
   const long long start = quotient(total * blockIdx.x, ctas), end = quotient(total * (blockIdx.x + 1), ctas);
   if (before <= start && start < before + mine * g.n_kv_heads) {

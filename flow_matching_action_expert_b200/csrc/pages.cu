@@ -71,10 +71,10 @@ __device__ __forceinline__ int owner(const int *cum, int n, int i) {
 // read it instead of in the free list (pages pushed in this step lie at or above the old top, so
 // the pushes never touch an entry a pop reads).
 //
-// A decode step is one CTA: a chain of two scans and three dependent loads.  With more rows every
+// A decode step is one CTA: a chain of three scans and three dependent loads.  With more rows every
 // CTA repeats the scans and takes a share of the rows and pages; the last one to finish writes the
 // lengths and the new top, which the others still read (they may be updated in place).  Measured:
-// 64 requests of one token 4.7 us; 2000 requests and 91 thousand rows 13.6 us (one CTA: 1173 us).
+// 64 requests of one token 4.8 us; 2000 requests and 91 thousand rows 13.9 us (one CTA: 1173 us).
 template <int PT>
 __global__ void __launch_bounds__(PT) k_pages_plan(PlanParams p) {
   extern __shared__ int sm[];
@@ -164,7 +164,7 @@ __global__ void __launch_bounds__(PT) k_pages_plan(PlanParams p) {
   }
   for (int e = first; e < n_back; e += stride) {
     const int page = given_back(e);
-    bad |= page < 0 || page >= g.n_pages;
+    bad |= !pg_in_pool(page, g);
     p.free_pages[nf + e] = page;
   }
   for (int r = first; r < p.n_rows; r += stride) {
@@ -175,7 +175,7 @@ __global__ void __launch_bounds__(PT) k_pages_plan(PlanParams p) {
         pos = len + (r - s_rows[b]);
         const int e = pos >> g.shift, held = pg_pages(len, g);
         const int page = e < held ? p.table[(size_t)b * g.width + e] : popped(s_take[b] + e - held);
-        if (page >= 0 && page < g.n_pages) {
+        if (pg_in_pool(page, g)) {
           slot = (page << g.shift) + (pos & ((1 << g.shift) - 1));
         } else {
           bad = true;
@@ -569,7 +569,7 @@ __global__ void __cluster_dims__(SC, 1, 1) __launch_bounds__(ST, 2) k_pages_sele
     for (int c0 = my_c0; c0 < n; c0 += SC * (ST / 32) * RUN) {
       int mine = c0 == my_c0 ? raw_page : lane < RUN && c0 + lane < n ? row[lo + c0 + lane] : -1;
       if (lane >= RUN || c0 + lane >= n) mine = -1;
-      else if (mine < 0 || mine >= g.n_pages) {
+      else if (!pg_in_pool(mine, g)) {
         bad = true;
         mine = -1;
       }

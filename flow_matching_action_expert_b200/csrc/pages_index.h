@@ -1,7 +1,7 @@
-// Index arithmetic of the paged KV cache.  Every address the kernels form from a value that came
-// from device memory (a length, a page number, a slot, a chosen page) goes through one of these
-// functions, which return -1 (or a clamped length) for anything out of range.  Plain C++ as well,
-// so that the bounds are tested on the CPU.
+// Index arithmetic of the paged KV cache.  Every value from device memory that the kernels form an
+// address of (a length, a page number, a slot, a chosen page) is checked by one of these functions,
+// which return false, -1 or a clamped length for anything out of range.  Plain C++ as well, so that
+// the bounds are tested on the CPU.
 #pragma once
 
 #include <stdint.h>
@@ -36,11 +36,14 @@ PG_HD int pg_len(int len, const PageGeom &g, bool *bad) {
 // Pages that hold `n` tokens (0 <= n <= 2^24).
 PG_HD int pg_pages(int n, const PageGeom &g) { return (n + (1 << g.shift) - 1) >> g.shift; }
 
+// Is `page` a page of the pool?
+PG_HD bool pg_in_pool(int page, const PageGeom &g) { return page >= 0 && page < g.n_pages; }
+
 // Physical page of entry `e` of a table row, -1 when the entry or its content is out of range.
 PG_HD int pg_page(const int32_t *row, int e, const PageGeom &g) {
   if (e < 0 || e >= g.width) return -1;
   const int p = row[e];
-  return p >= 0 && p < g.n_pages ? p : -1;
+  return pg_in_pool(p, g) ? p : -1;
 }
 
 // Keys that a request's `len` tokens give when it attends to `n_sel` of its pages (no list: all).

@@ -24,10 +24,10 @@
 // go to k_pages_attend_cluster, which joins through shared memory.
 //
 // Measured: 64 requests of up to 32768 tokens, 8 heads of 256 on one KV head (1.13 GB of K and V),
-// 177 to 181 us, 6.3 TB/s, 96% of the GPU's measured copy rate; 24 ragged requests, 32/8 heads of 128
+// 179 to 181 us, 6.3 TB/s, 96% of the GPU's measured copy rate; 24 ragged requests, 32/8 heads of 128
 // in f16 (351 MB) 65 us, 5.4 TB/s; one request of 131071 tokens (134 MB) 33 us, of which the reading
 // takes 21 and the start, the last tiles and the join the rest.  Short calls are latency: 7.9 us
-// for one request of 544 tokens, 9.8 for 16 of 800.
+// for one request of 544 tokens, 9.9 for 16 of 800.
 //
 // Weights are split into two 16-bit parts, p = hi + lo, and multiplied twice: the products cost
 // nothing next to the loads, and the weights then count to 2^-16 (bf16) or 2^-22 (f16) instead of
@@ -674,7 +674,9 @@ cudaError_t attend(const PagedAttnParams &p, int sm_count, cudaStream_t st) {
   // chunks where an even split over the whole wave gives fewer; one more costs 1.4 us at d = 256 and
   // 0.8 below.  One request of 1000 tokens: 7.5 us (split 8.1), of 2000: 10.4 (8.7) at d = 256, 8.0
   // (8.3) at d = 128; 16 requests of 1000: 10.1 (12.7).  Past half a wave clusters no longer fit at once
-  // (37 requests of 1000: 20.3, split 17.6).
+  // (37 requests of 1000: 20.3, split 17.6).  The lengths are on the GPU, so the rule goes by what the
+  // table rows or the lists have room for; the figures are for rows just as long as the requests.  With
+  // rows for 8192 tokens one request of 544 takes the split form and 0.9 us more, 16 of 800 1.0 more.
   const long long most_c = (chunks + CLUSTER - 1) / CLUSTER, most_s = (pairs * (chunks + SETUP) + wave - 1) / wave;
   if (pairs * CLUSTER * 2 <= wave && most_c - most_s <= (D == 256 ? 1 : 3)) {
     cfg.gridDim = dim3(CLUSTER, p.g.n_kv_heads, p.batch);

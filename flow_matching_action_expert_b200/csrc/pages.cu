@@ -74,7 +74,7 @@ __device__ __forceinline__ int owner(const int *cum, int n, int i) {
 // A decode step is one CTA: a chain of three scans and three dependent loads.  With more rows every
 // CTA repeats the scans and takes a share of the rows and pages; the last one to finish writes the
 // lengths and the new top, which the others still read (they may be updated in place).  Measured:
-// 64 requests of one token 4.8 us; 2000 requests and 91 thousand rows 13.9 us (one CTA: 1173 us).
+// 64 requests of one token 4.9 us; 2000 requests and 91 thousand rows 13.9 us (one CTA: 1173 us).
 template <int PT>
 __global__ void __launch_bounds__(PT) k_pages_plan(PlanParams p) {
   extern __shared__ int sm[];
@@ -282,7 +282,7 @@ __device__ __forceinline__ void rotate8(float (&x1)[8], float (&x2)[8], const fl
 
 // Moves bytes: a row is read once and written once, with two table rows of 8 bytes per pair that
 // its heads share through L1.  A thread takes eight pairs (16 bytes of each half) of HEADS heads.
-// Measured: 4348 rows of 10 heads of 256 (44 MB) 13 us, 3.4 TB/s: two waves of CTAs, each as long as
+// Measured: 4348 rows of 10 heads of 256 (44 MB) 13.8 us, 3.2 TB/s: two waves of CTAs, each as long as
 // its chain of loads (slot, then table row); 9465 rows 23.6 us, 4.1 TB/s.  Two heads per thread take
 // 13.6 us; 64 registers instead of 80 spill (14.9).  A decode step of 16 rows: 4.3 us.
 // The first CTAs look for rows that fill their page, one KV head each, several small pages at a time; a

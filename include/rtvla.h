@@ -433,10 +433,13 @@ void rtvla_vision_destroy(rtvla_vision_ctx *ctx);
 /* =========================================================================================
  * Paged KV cache: one pool of fixed-size pages shared by requests of different length, the
  * bookkeeping that hands its pages out, and the attention of one new token per request over it.
- * The pages' pipeline fills a contiguous rtvla_kv once and attends into it; these calls serve
- * what comes next to that: text decoding of the prefix model, an observation appended to a
- * prefix, robots with long histories that share one GPU's memory (integration aids of this
- * library; the paper has no counterpart).  A context of its own, with the conventions above
+ * The calls above fill a contiguous rtvla_kv once and attend into it; these serve what comes next
+ * to that: decoding steps of the prefix model (up to its residual stream; embedding lookup, final norm
+ * and vocabulary product are the caller's) and requests with long histories that share one GPU's memory
+ * (integration aids of this library; the paper has no counterpart).  A query sees the tokens that its
+ * request holds when it is run, so tokens added one at a time do not see what comes after them:
+ * rtvla_prefill, whose attention runs both ways over the prefix, computes something else for the same
+ * tokens given together.  A context of its own, with the conventions above
  * (contiguous row-major tensors, asynchronous calls on `stream`, device-detected errors through
  * a sync call; calls on one context must not overlap on the GPU).
  *
@@ -480,7 +483,8 @@ typedef struct {
   void *k;         /* [n_layers][n_pages][n_kv_heads][page_size][head_dim] */
   void *v;         /* the same */
   void *k_mean;    /* [n_layers][n_pages][n_kv_heads][head_dim]: mean key of every full page; may be
-                      null when rtvla_pages_select is not used */
+                      null when rtvla_pages_select is not used.  Only rtvla_pages_write computes it:
+                      pages filled otherwise (rtvla_prefill, a copy) have what the caller puts there */
   int32_t *table;  /* [batch][table_width] */
   int32_t *lens;   /* [batch] tokens each request holds, 0..table_width * page_size */
   int batch;       /* 1..max_batch */
